@@ -12,6 +12,12 @@ Entry points (same names as the C ABI):
   gdr2_bwd_chunked_recompute(q, k, v, log_alpha, b, w, dO, S0=None, dS_T=None) -> grads
   gdr2_decode_step(q, k, v, log_alpha, b, w, S_in=None, S_out=None)
   gdr2_out_gate_fwd(o, g, weight, eps) / gdr2_out_gate_bwd(o, g, weight, dy, eps)
+Around the mixer, in a hybrid stack:
+  gdr2_layer_norm_fwd(x, weight, bias) -> (y, mean, rstd) / gdr2_layer_norm_bwd(x, weight, mean, rstd, dy)
+  gdr2_swa_fwd(q, k, v, window, sinks) -> (o, lse) / gdr2_swa_bwd(q, k, v, o, lse, dO, window, sinks)
+  gdr2_swa_cache_fill(k, v, k_cache, v_cache, sinks) / gdr2_swa_decode_step(q, k, v, k_cache, v_cache, pos, sinks)
+  gdr2_glr_fwd(x, log_a, h0) -> (h, h_T, fwd_ws) / gdr2_glr_bwd(x, log_a, dh, fwd_ws, dh_T)
+  gdr2_glr_step(x, log_a, h_in, h_out)
 Each of b, w and log_alpha may be channel-wise ([..., d]) or a scalar per head (the token shape of
 q without its channel axis); the gate-shape bits passed to the *_ex entry points follow from the
 shapes, and the gradients come back in the shape of their gate.  ``prologue=Prologue(c, eps)``
@@ -33,7 +39,11 @@ __all__ = ["gdr2_fwd_chunked", "gdr2_bwd_chunked", "gdr2_decode_step", "gdr2_fwd
            "gdr2_fwd_carry", "gdr2_bwd_state", "gdr2_bwd_grads", "fwd_workspace_bytes",
            "bwd_workspace_bytes", "library_path", "load_library", "Gdr2Error", "CHUNK", "gate_bits",
            "ERASE_SCALAR", "WRITE_SCALAR", "DECAY_SCALAR", "gdr2_out_gate_fwd", "gdr2_out_gate_bwd",
-           "Prologue"]
+           "Prologue", "gdr2_layer_norm_fwd", "gdr2_layer_norm_bwd", "gdr2_glr_fwd", "gdr2_glr_bwd",
+           "gdr2_glr_step", "gdr2_swa_fwd", "gdr2_swa_bwd", "gdr2_swa_cache_fill",
+           "gdr2_swa_decode_step", "glr_fwd_workspace_bytes", "glr_bwd_workspace_bytes",
+           "layer_norm_bwd_workspace_bytes", "swa_bwd_workspace_bytes",
+           "swa_decode_workspace_bytes"]
 
 CHUNK = 64
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -136,6 +146,23 @@ def load_library():
     lib.gdr2_out_gate_bwd.restype = ctypes.c_int
     lib.gdr2_out_gate_bwd_workspace_bytes.argtypes = [I64, I64]
     lib.gdr2_out_gate_bwd_workspace_bytes.restype = SZ
+    I = ctypes.c_int
+    for name, args in (
+            ("gdr2_layer_norm_fwd", [I64, I64, I, P, P, P, F, P, P, P, P]),
+            ("gdr2_layer_norm_bwd", [I64, I64, I] + [P] * 9 + [SZ, P]),
+            ("gdr2_glr_fwd", [I64] * 3 + [I] + [P] * 6 + [SZ, P]),
+            ("gdr2_glr_bwd", [I64] * 3 + [I, P, P, P, SZ] + [P] * 6 + [SZ, P]),
+            ("gdr2_glr_step", [I64, I64, I] + [P] * 6),
+            ("gdr2_swa_fwd", [I64] * 5 + [I, I64, I64, F] + [P] * 7),
+            ("gdr2_swa_bwd", [I64] * 5 + [I, I64, I64, F] + [P] * 11 + [SZ, P]),
+            ("gdr2_swa_cache_fill", [I64] * 4 + [I, I64, I64] + [P] * 6),
+            ("gdr2_swa_decode_step", [I64] * 4 + [I, I64, I64, F] + [P] * 8 + [SZ, P])):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = I
+    for name, n in (("gdr2_layer_norm_bwd", 2), ("gdr2_glr_fwd", 3), ("gdr2_glr_bwd", 3),
+                    ("gdr2_swa_bwd", 7), ("gdr2_swa_decode", 6)):
+        getattr(lib, name + "_workspace_bytes").argtypes = [I64] * n
+        getattr(lib, name + "_workspace_bytes").restype = SZ
     lib.gdr2_fwd_workspace_bytes.argtypes = [I64] * 5 + [ctypes.c_int]
     lib.gdr2_fwd_workspace_bytes.restype = SZ
     lib.gdr2_bwd_workspace_bytes.argtypes = [I64] * 5 + [ctypes.c_int]
@@ -536,3 +563,250 @@ def gdr2_out_gate_bwd(o, g, weight, dy, eps=1e-6, workspace=None):
          _ptr(weight), float(eps), _ptr(dy), _ptr(out["do"]), _ptr(out["dg"]),
          _ptr(out["dweight"]), _ptr(ws), ws.numel())
     return out
+
+
+# ---------------------------------------------------------------------------------------------
+# Operators around the mixer.
+def _new_ws(workspace, need, dev):
+    if workspace is not None:
+        return workspace
+    return torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+
+
+def _need_tensor(name, t, ndim=None):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if ndim is not None and t.dim() != ndim:
+        raise ValueError(f"{name} must be a {ndim}-D tensor")
+
+
+def layer_norm_bwd_workspace_bytes(rows, D):
+    return load_library().gdr2_layer_norm_bwd_workspace_bytes(rows, D)
+
+
+def glr_fwd_workspace_bytes(B, T, D):
+    return load_library().gdr2_glr_fwd_workspace_bytes(B, T, D)
+
+
+def glr_bwd_workspace_bytes(B, T, D):
+    return load_library().gdr2_glr_bwd_workspace_bytes(B, T, D)
+
+
+def swa_bwd_workspace_bytes(B, T, H, Hkv, d, window, sinks=0):
+    return load_library().gdr2_swa_bwd_workspace_bytes(B, T, H, Hkv, d, window, sinks)
+
+
+def swa_decode_workspace_bytes(N, H, Hkv, d, window, sinks=0):
+    return load_library().gdr2_swa_decode_workspace_bytes(N, H, Hkv, d, window, sinks)
+
+
+def _norm_inputs(x, weight):
+    _need_tensor("x", x)
+    if x.dim() < 1:
+        raise ValueError("x must be a tensor [..., D]")
+    _dtype(x)
+    dev, D = x.device, x.shape[-1]
+    _need("x", x, x.shape, x.dtype, dev)
+    _need("weight", weight, (D,), torch.float32, dev)
+    return dev, (x.numel() // D if D else 0), D
+
+
+def gdr2_layer_norm_fwd(x, weight, bias=None, eps=1e-5):
+    """Layer norm over the last axis of x [..., D] (D a multiple of 8, up to 16384), weight and bias
+    [D] fp32.  Returns (y, mean, rstd), the statistics [...] in fp32 for the backward."""
+    lib = load_library()
+    dev, rows, D = _norm_inputs(x, weight)
+    _need("bias", bias, (D,), torch.float32, dev, optional=True)
+    _on_gpu(dev)
+    y = torch.empty_like(x)
+    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    rstd = torch.empty_like(mean)
+    _run("gdr2_layer_norm_fwd", dev, lib.gdr2_layer_norm_fwd, rows, D, _dtype(x), _ptr(x), _ptr(weight),
+         _ptr(bias), float(eps), _ptr(y), _ptr(mean), _ptr(rstd))
+    return y, mean, rstd
+
+
+def gdr2_layer_norm_bwd(x, weight, mean, rstd, dy, want_dbias=True, workspace=None):
+    """Backward of gdr2_layer_norm_fwd for the cotangent dy, with the forward's mean and rstd.
+    Returns dict dx, dweight, dbias (None if not wanted)."""
+    lib = load_library()
+    dev, rows, D = _norm_inputs(x, weight)
+    _need("mean", mean, x.shape[:-1], torch.float32, dev)
+    _need("rstd", rstd, x.shape[:-1], torch.float32, dev)
+    _need("dy", dy, x.shape, x.dtype, dev)
+    if workspace is not None:
+        _ws("workspace", workspace, dev)
+    _on_gpu(dev)
+    ws = _new_ws(workspace, lib.gdr2_layer_norm_bwd_workspace_bytes(rows, D), dev)
+    g = dict(dx=torch.empty_like(x), dweight=torch.empty_like(weight),
+             dbias=torch.empty_like(weight) if want_dbias else None)
+    _run("gdr2_layer_norm_bwd", dev, lib.gdr2_layer_norm_bwd, rows, D, _dtype(x), _ptr(x), _ptr(weight),
+         _ptr(mean), _ptr(rstd), _ptr(dy), _ptr(g["dx"]), _ptr(g["dweight"]), _ptr(g["dbias"]), _ptr(ws), ws.numel())
+    return g
+
+
+def _glr_inputs(x, log_a, ndim):
+    _need_tensor("x", x, ndim)
+    _dtype(x)
+    dev = x.device
+    _need("x", x, x.shape, x.dtype, dev)
+    _need("log_a", log_a, x.shape, torch.float32, dev)
+    return dev
+
+
+def gdr2_glr_fwd(x, log_a, h0=None, want_final_state=True, workspace=None):
+    """Gated linear recurrence h_t = exp(log_a_t) h_{t-1} + x_t per channel of x [B, T, D] (D a
+    multiple of 8); log_a fp32, h0 [B, D] fp32.  Returns (h, h_T or None, fwd_ws); fwd_ws is what
+    gdr2_glr_bwd needs.  ``workspace`` may pass a preallocated uint8 device tensor of at least
+    glr_fwd_workspace_bytes(B, T, D) bytes."""
+    lib = load_library()
+    dev = _glr_inputs(x, log_a, 3)
+    B, T, D = x.shape
+    _need("h0", h0, (B, D), torch.float32, dev, optional=True)
+    if workspace is not None:
+        _ws("workspace", workspace, dev)
+    _on_gpu(dev)
+    h = torch.empty_like(x)
+    hT = torch.empty((B, D), dtype=torch.float32, device=dev) if want_final_state else None
+    ws = _new_ws(workspace, lib.gdr2_glr_fwd_workspace_bytes(B, T, D), dev)
+    _run("gdr2_glr_fwd", dev, lib.gdr2_glr_fwd, B, T, D, _dtype(x), _ptr(x), _ptr(log_a), _ptr(h0), _ptr(h),
+         _ptr(hT), _ptr(ws), ws.numel())
+    return h, hT, ws
+
+
+def gdr2_glr_bwd(x, log_a, dh, fwd_ws, dh_T=None, want_dh0=True, workspace=None):
+    """Backward of gdr2_glr_fwd for the cotangents dh (of h) and dh_T (of h_T); ``fwd_ws`` is the
+    third result of the forward on the same inputs.  Returns dict dx, dlog_a, dh0 (None if not
+    wanted)."""
+    lib = load_library()
+    dev = _glr_inputs(x, log_a, 3)
+    B, T, D = x.shape
+    _need("dh", dh, x.shape, x.dtype, dev)
+    _need("dh_T", dh_T, (B, D), torch.float32, dev, optional=True)
+    _ws("fwd_ws", fwd_ws, dev)
+    if workspace is not None:
+        _ws("workspace", workspace, dev)
+    _on_gpu(dev)
+    g = dict(dx=torch.empty_like(x), dlog_a=torch.empty_like(log_a),
+             dh0=torch.empty((B, D), dtype=torch.float32, device=dev) if want_dh0 else None)
+    ws = _new_ws(workspace, lib.gdr2_glr_bwd_workspace_bytes(B, T, D), dev)
+    _run("gdr2_glr_bwd", dev, lib.gdr2_glr_bwd, B, T, D, _dtype(x), _ptr(x), _ptr(log_a), _ptr(fwd_ws),
+         fwd_ws.numel(), _ptr(dh), _ptr(dh_T), _ptr(g["dx"]), _ptr(g["dlog_a"]), _ptr(g["dh0"]), _ptr(ws), ws.numel())
+    return g
+
+
+def gdr2_glr_step(x, log_a, h_in=None, h_out=None):
+    """One token of the recurrence for N sequences: x [N, D], log_a [N, D] fp32, state [N, D] fp32.
+    h_out defaults to h_in (in place) or a new buffer.  Returns (h in x's dtype, h_out)."""
+    lib = load_library()
+    dev = _glr_inputs(x, log_a, 2)
+    _need("h_in", h_in, x.shape, torch.float32, dev, optional=True)
+    _need("h_out", h_out, x.shape, torch.float32, dev, optional=True)
+    _on_gpu(dev)
+    if h_out is None:
+        h_out = h_in if h_in is not None else torch.empty(x.shape, dtype=torch.float32, device=dev)
+    h = torch.empty_like(x)
+    _run("gdr2_glr_step", dev, lib.gdr2_glr_step, x.shape[0], x.shape[1], _dtype(x), _ptr(x), _ptr(log_a),
+         _ptr(h_in), _ptr(h_out), _ptr(h))
+    return h, h_out
+
+
+def _swa_inputs(q, k, v, ndim):
+    _need_tensor("q", q, ndim)
+    _need_tensor("k", k, ndim)
+    _dtype(q)
+    dev = q.device
+    _need("q", q, q.shape, q.dtype, dev)
+    _need("k", k, q.shape[:-2] + (k.shape[-2], q.shape[-1]), q.dtype, dev)
+    _need("v", v, k.shape, q.dtype, dev)
+    return dev
+
+
+def _swa_scale(scale, d):
+    return float(d) ** -0.5 if scale is None else float(scale)
+
+
+def gdr2_swa_fwd(q, k, v, window, sinks=0, scale=None, lengths=None):
+    """Causal attention over the last ``window`` tokens and the first ``sinks`` (0..64) tokens:
+    q [B, T, H, d], k and v [B, T, Hkv, d] (H a multiple of Hkv, d in {64, 128}); scale defaults to
+    d^-0.5.  ``lengths`` [B] int32 marks rows at and behind a sequence's length as padding (o zero,
+    lse -inf there).  Returns (o, lse [B, H, T] fp32)."""
+    lib = load_library()
+    dev = _swa_inputs(q, k, v, 4)
+    B, T, H, d = q.shape
+    _need("lengths", lengths, (B,), torch.int32, dev, optional=True)
+    _on_gpu(dev)
+    o = torch.empty_like(q)
+    lse = torch.empty((B, H, T), dtype=torch.float32, device=dev)
+    _run("gdr2_swa_fwd", dev, lib.gdr2_swa_fwd, B, T, H, k.shape[2], d, _dtype(q), int(window), int(sinks),
+         _swa_scale(scale, d), _ptr(q), _ptr(k), _ptr(v), _ptr(lengths), _ptr(o), _ptr(lse))
+    return o, lse
+
+
+def gdr2_swa_bwd(q, k, v, o, lse, dO, window, sinks=0, scale=None, lengths=None, workspace=None):
+    """Backward of gdr2_swa_fwd for the cotangent dO, with the forward's o and lse and the same
+    window, sinks, scale and lengths.  Returns dict dq, dk, dv."""
+    lib = load_library()
+    dev = _swa_inputs(q, k, v, 4)
+    B, T, H, d = q.shape
+    _need("o", o, q.shape, q.dtype, dev)
+    _need("lse", lse, (B, H, T), torch.float32, dev)
+    _need("dO", dO, q.shape, q.dtype, dev)
+    _need("lengths", lengths, (B,), torch.int32, dev, optional=True)
+    if workspace is not None:
+        _ws("workspace", workspace, dev)
+    _on_gpu(dev)
+    window, sinks = int(window), int(sinks)
+    g = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v))
+    ws = _new_ws(workspace, lib.gdr2_swa_bwd_workspace_bytes(B, T, H, k.shape[2], d, window, sinks), dev)
+    _run("gdr2_swa_bwd", dev, lib.gdr2_swa_bwd, B, T, H, k.shape[2], d, _dtype(q), window, sinks,
+         _swa_scale(scale, d), _ptr(q), _ptr(k), _ptr(v), _ptr(lengths), _ptr(o), _ptr(lse), _ptr(dO), _ptr(g["dq"]),
+         _ptr(g["dk"]), _ptr(g["dv"]), _ptr(ws), ws.numel())
+    return g
+
+
+def _swa_cache(k, k_cache, v_cache, sinks, dev):
+    """Checks the caches [N, sinks + window, Hkv, d] against k [N, ..., Hkv, d]; returns window."""
+    _need_tensor("k_cache", k_cache, 4)
+    shape = (k.shape[0], k_cache.shape[1], k.shape[-2], k.shape[-1])
+    _need("k_cache", k_cache, shape, k.dtype, dev)
+    _need("v_cache", v_cache, shape, k.dtype, dev)
+    return k_cache.shape[1] - sinks
+
+
+def gdr2_swa_cache_fill(k, v, k_cache, v_cache, sinks=0, lengths=None):
+    """Stores what decoding may still see of a prefill's k and v [B, T, Hkv, d] (sequence b has
+    lengths[b] tokens, T without ``lengths``) in the bounded caches [B, sinks + window, Hkv, d];
+    slots no position lives in keep their contents.  The next token's position is the length."""
+    lib = load_library()
+    dev = _swa_inputs(k, k, v, 4)
+    B, T, Hkv, d = k.shape
+    _need("lengths", lengths, (B,), torch.int32, dev, optional=True)
+    window = _swa_cache(k, k_cache, v_cache, int(sinks), dev)
+    _on_gpu(dev)
+    _run("gdr2_swa_cache_fill", dev, lib.gdr2_swa_cache_fill, B, T, Hkv, d, _dtype(k), window, int(sinks), _ptr(k),
+         _ptr(v), _ptr(lengths), _ptr(k_cache), _ptr(v_cache))
+
+
+def gdr2_swa_decode_step(q, k, v, k_cache, v_cache, pos, sinks=0, scale=None, workspace=None):
+    """One token per sequence: q [N, H, d], k and v [N, Hkv, d] at position pos [N] int32 (negative: no
+    token, o = 0).  Stores k and v in the bounded caches [N, sinks + window, Hkv, d] (in place) and
+    returns o [N, H, d] over the positions the window and the sinks leave visible."""
+    lib = load_library()
+    dev = _swa_inputs(q, k, v, 3)
+    N, H, d = q.shape
+    sinks = int(sinks)
+    _need("pos", pos, (N,), torch.int32, dev)
+    window = _swa_cache(k, k_cache, v_cache, sinks, dev)
+    if workspace is not None:
+        _ws("workspace", workspace, dev)
+    _on_gpu(dev)
+    o = torch.empty_like(q)
+    ws = workspace
+    if ws is None:
+        need = lib.gdr2_swa_decode_workspace_bytes(N, H, k.shape[1], d, window, sinks)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    _run("gdr2_swa_decode_step", dev, lib.gdr2_swa_decode_step, N, H, k.shape[1], d, _dtype(q), window, sinks,
+         _swa_scale(scale, d), _ptr(q), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(pos), _ptr(o), _ptr(ws),
+         ws.numel() if ws is not None else 0)
+    return o

@@ -13,7 +13,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgdr2.so")
 OBJ_DIR = os.path.join(PKG, "_build")
 SOURCES = ["gdr2_api.hip", "gdr2_wy.hip", "gdr2_fwd.hip", "gdr2_bwd.hip", "gdr2_decode.hip",
-           "gdr2_epilogue.hip"]
+           "gdr2_epilogue.hip", "gdr2_block_api.hip", "gdr2_norm.hip", "gdr2_glr.hip",
+           "gdr2_swa_fwd.hip", "gdr2_swa_bwd.hip", "gdr2_swa_decode.hip"]
 ARCH = "gfx950"
 FLAGS = ["-O3", "-std=c++17", f"--offload-arch={ARCH}", "-fPIC", "-I", INCLUDE, "-I", CSRC,
          "-Wall", "-Wshadow", "-Wno-unused-function",

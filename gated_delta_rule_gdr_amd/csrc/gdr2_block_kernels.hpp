@@ -1,0 +1,121 @@
+// gdr2_block_kernels.hpp -- host-side launch interface of the operators around the GDR-2 mixer:
+// layer norm, gated linear recurrence, sliding-window attention and its decode.
+#pragma once
+#include <hip/hip_runtime.h>
+
+namespace gdr2 {
+
+// Layer norm over the last axis: y = (x - mean) rstd weight + bias per row of D channels.
+struct NormParams {
+    long rows;
+    int D;
+    float eps;
+    const void* x;        // [rows][D] input dtype
+    const float* weight;  // [D]
+    const float* bias;    // [D] or null
+    void* y;              // forward output [rows][D]
+    float *mean, *rstd;   // [rows] fp32: forward outputs (null = not wanted), backward inputs
+    const void* dy;       // backward: cotangent of y
+    void* dx;             // backward output [rows][D]
+    float *dweight, *dbias;  // backward outputs [D] (dbias null = not wanted)
+    float* part;          // backward workspace [norm_bwd_blocks(rows, D)][2][D] fp32
+};
+constexpr int kNormMaxD = 16384;
+long norm_bwd_blocks(long rows, int D);
+hipError_t norm_dispatch(int dtype_bf16, bool bwd, const NormParams& p, hipStream_t s);
+
+// Gated linear recurrence h_t = exp(log_a_t) h_{t-1} + x_t per channel.
+constexpr int kGlrSeg = 128;    // tokens of a segment: one workgroup's share of the time axis
+constexpr int kGlrCh = 64;      // channels of a workgroup
+constexpr int kGlrGroup = 16;   // segments between two published running states
+struct GlrParams {
+    int B, nseg, nstrip;
+    long T, D;
+    const void* x;        // [B][T][D] input dtype
+    const float* la;      // [B][T][D]
+    const float* h0;      // [B][D] or null
+    void* h;              // [B][T][D] input dtype
+    float* hT;            // [B][D] or null
+    float* states;        // [B][nseg][D]: the state entering each segment
+    const void* dh;       // backward: cotangent of h
+    const float* dhT;     // [B][D] or null
+    void* dx;             // [B][T][D] input dtype
+    float* dla;           // [B][T][D]
+    float* dh0;           // [B][D] or null
+    unsigned long long* pub;  // [B][nseg][nstrip * kGlrCh] published segment maps, then
+                              // [B][nseg / kGlrGroup][..] published running states
+    unsigned* ticket;
+};
+inline long glr_segments(long T) { return T <= 0 ? 1 : (T + kGlrSeg - 1) / kGlrSeg; }
+inline long glr_strips(long D) { return (D + kGlrCh - 1) / kGlrCh; }
+hipError_t glr_dispatch(int dtype_bf16, bool bwd, const GlrParams& p, hipStream_t s);
+struct GlrStepParams {
+    long n;               // N * D elements
+    const void* x;
+    const float* la;
+    const float* h_in;    // may equal h_out; null = zero state
+    float* h_out;
+    void* h;
+};
+hipError_t glr_step_dispatch(int dtype_bf16, const GlrStepParams& p, hipStream_t s);
+
+// Sliding-window attention with sinks: query i of a sequence of L tokens sees key j when
+// j <= i < L and (i - j < window or j < sinks).
+constexpr int kSwaMaxSinks = 64;
+constexpr int kSwaKeyTile = 128;    // keys of a key/value-gradient workgroup
+constexpr int kSwaSinkPieces = 16;  // at most this many pieces of the queries behind the window
+struct SwaParams {
+    int B, H, Hkv, d, sinks;
+    long T, window;         // window <= T
+    float scale;
+    const void *q, *k, *v;  // [B][T][H][d], [B][T][Hkv][d]
+    const int* lengths;     // [B] or null (every sequence has T tokens)
+    void* o;                // [B][T][H][d] (forward output, backward input)
+    float* lse;             // [B][H][T] log of the softmax denominators (natural; -inf: nothing seen)
+    const void* dO;         // backward
+    void *dq, *dk, *dv;
+    float* delta;           // [B][H][T] sum of dO o per query (backward workspace)
+    float* sink_part;       // [pieces][B][Hkv][2][64][d] dk, dv of the sinks from far queries
+    int pieces;             // 0: no query lies behind the window, or no sinks
+    long far0, piece_len;   // piece i covers queries far0 + i * piece_len ..
+};
+// Pieces of the far queries (those the first key tile's workgroup does not walk) for sinks > 0.
+struct SwaFar {
+    int pieces;
+    long far0, piece_len;
+};
+inline SwaFar swa_far(long T, long window, int sinks) {
+    const long far0 = (kSwaKeyTile - 1 + window + 63) / 64 * 64;
+    if (sinks <= 0 || T <= far0) return {0, far0, 0};
+    long len = ((T - far0 + kSwaSinkPieces - 1) / kSwaSinkPieces + 63) / 64 * 64;
+    if (len < 512) len = 512;
+    return {(int)((T - far0 + len - 1) / len), far0, len};
+}
+hipError_t swa_fwd_dispatch(int dtype_bf16, const SwaParams& p, hipStream_t s);
+hipError_t swa_bwd_dispatch(int dtype_bf16, const SwaParams& p, hipStream_t s);
+
+// The bounded cache: [N][sinks + window][Hkv][d]; position p lives in slot p (p < sinks) or
+// sinks + (p - sinks) mod window.
+struct SwaFillParams {
+    int B, Hkv, sinks;
+    long T, window, row16;  // row16: 16-byte pieces of a token's row (all heads)
+    const void *k, *v;      // [B][T][Hkv][d]
+    void *kc, *vc;
+    const int* lengths;
+};
+hipError_t swa_fill_dispatch(const SwaFillParams& p, hipStream_t s);
+struct SwaDecodeParams {
+    int N, H, Hkv, d, sinks;
+    long window;
+    float scale;
+    const void *q, *k, *v;  // [N][H][d], [N][Hkv][d]
+    void *kc, *vc;
+    const int* pos;         // [N] position of the new token; negative: no token
+    void* o;                // [N][H][d]
+    int splits;             // parts of the slots per (sequence, key/value head, head group)
+    float* part;            // splits > 1: [N][Hkv][groups][splits][16][d + 2] fp32
+};
+int swa_decode_splits(long N, long Hkv, long groups, long slots);
+hipError_t swa_decode_dispatch(int dtype_bf16, const SwaDecodeParams& p, hipStream_t s);
+
+}  // namespace gdr2

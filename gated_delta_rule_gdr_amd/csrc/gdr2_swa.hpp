@@ -1,0 +1,170 @@
+// gdr2_swa.hpp -- tiles and products of the sliding-window attention kernels (gfx950).
+//
+// Every product runs on 32x32 MFMA with fp32 accumulators (bf16: v_mfma_f32_32x32x16_bf16, fp32:
+// v_mfma_f32_32x32x2_f32).  Lane l = 32 h + n holds, of a 32x32 product C = A B,
+//     C: column n, rows crow(r, h) = 8 (r / 4) + 4 h + r % 4 for its sixteen registers r
+//     A: row n, B: column n; the contraction values of half h.
+// Scores are formed with the side that is reduced over in the rows (keys for o and dq, queries for
+// dk and dv), so that the probabilities a lane holds are contraction values of the next product's B
+// operand as they stand: sixteen registers are rows 16 kk + {4h..4h+3, 8+4h..8+4h+3}, kk = 0, 1,
+// and its A operand is gathered from the LDS tile in that same order (ds_read_b64_tr_b16 for bf16,
+// one float per register for fp32).  No probability ever crosses lanes.
+//
+// An LDS tile is `rows` x CPR 16-byte pieces; piece c of row r sits at place c ^ swz(r), so that
+// neither sixteen rows read at one piece nor four rows read across 64 bytes share banks.
+#pragma once
+#include "gdr2_block_kernels.hpp"
+#include "gdr2_common.hpp"
+
+namespace gdr2 {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+constexpr int kSwaThreads = 256, kSwaWaves = 4;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLowest = -3.0e38f;
+
+__device__ __forceinline__ int crow(int r, int h) { return 8 * (r / 4) + 4 * h + r % 4; }
+__device__ __forceinline__ float exp2_f(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ f32x16 zero16() {
+    return f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+}
+
+template <typename T, int D>
+struct Swa {
+    static constexpr int ES = (int)sizeof(T), CPR = D * ES / 16;  // 16-byte pieces per row
+    static constexpr int KK = CPR / 2;                            // contraction steps of a row
+    static constexpr int DB = D / 32;                             // 32-column blocks of a row
+    static constexpr int BT = ES == 2 ? 64 : 32;                  // rows of a staged tile (16 KB at D = 128)
+    static constexpr int NB = BT / 32;
+    static constexpr int UNITS = BT * CPR / kSwaThreads;          // pieces a thread stages
+    static_assert(UNITS * kSwaThreads == BT * CPR, "staging");
+    typedef i32x4 tile[BT * CPR];
+
+    static __device__ __forceinline__ int swz(int row) {
+        if constexpr (CPR == 8) return ((row >> 1) & 1) << 2 | ((row >> 2) & 3);
+        else return (row & 3) << 2 | ((row >> 2) & 3);
+    }
+    static __device__ __forceinline__ int at(int row, int c) { return row * CPR + (c ^ swz(row)); }
+
+    // BT rows of a token tensor into registers: row r at base + r * stride bytes; rows at and
+    // behind `rows` are zero and not read
+    static __device__ __forceinline__ void fetch(i32x4 (&u)[UNITS], const char* base, long stride, int rows) {
+#pragma unroll
+        for (int i = 0; i < UNITS; ++i) {
+            const int x = threadIdx.x + i * kSwaThreads, r = x / CPR, c = x % CPR;
+            u[i] = r < rows ? *(const i32x4*)(base + r * stride + c * 16) : i32x4{0, 0, 0, 0};
+        }
+    }
+    static __device__ __forceinline__ void stage(i32x4* t, const i32x4 (&u)[UNITS]) {
+#pragma unroll
+        for (int i = 0; i < UNITS; ++i) {
+            const int x = threadIdx.x + i * kSwaThreads;
+            t[at(x / CPR, x % CPR)] = u[i];
+        }
+    }
+    // the B operand of 32 rows, kept in registers: piece 2 kk + h of the lane's row (null: zeros)
+    static __device__ __forceinline__ void keep(i32x4 (&f)[KK], const char* row) {
+        const int h = lane_id() >> 5;
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk)
+            f[kk] = row ? *(const i32x4*)(row + (2 * kk + h) * 16) : i32x4{0, 0, 0, 0};
+    }
+    static __device__ __forceinline__ void mma(f32x16& c, const i32x4& a, const i32x4& b) {
+        if constexpr (ES == 2) {
+            c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+        } else {
+            const f32x4 x = __builtin_bit_cast(f32x4, a), y = __builtin_bit_cast(f32x4, b);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(x[e], y[e], c, 0, 0, 0);
+        }
+    }
+    // rows r0 .. r0 + 31 of a tile times the kept rows: C[r][n] = tile row . kept row
+    static __device__ __forceinline__ f32x16 dots(const i32x4* t, int r0, const i32x4 (&f)[KK]) {
+        const int l = lane_id(), row = r0 + (l & 31), h = l >> 5;
+        f32x16 c = zero16();
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) mma(c, t[at(row, 2 * kk + h)], f[kk]);
+        return c;
+    }
+    // acc[db][d][n] += sum over the rows r0 + crow(r, h) of tile[row][32 db + d] w[r] (for bf16 the
+    // weights are rounded to bf16: the products' inputs, relative error 2^-8 each, summed in fp32)
+    static __device__ __forceinline__ void add_rows(f32x16 (&acc)[DB], const i32x4* t, int r0, const f32x16& w) {
+        const int l = lane_id(), h = l >> 5;
+        if constexpr (ES == 2) {
+            const int p = l & 15, sub = (l >> 4) & 1;
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                bf16x8 b;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) b[e] = (bf16)w[8 * kk + e];
+                const int ra = r0 + 16 * kk + 4 * h + (p >> 2), rb = ra + 8;
+#pragma unroll
+                for (int db = 0; db < DB; ++db) {
+                    const int c = 4 * db + 2 * sub + ((p & 3) >> 1);
+                    const bf16x4 lo = ds_read_tr4((const bf16*)(t + at(ra, c)) + 4 * (p & 1));
+                    const bf16x4 hi = ds_read_tr4((const bf16*)(t + at(rb, c)) + 4 * (p & 1));
+                    const bf16x8 a = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+                    acc[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc[db], 0, 0, 0);
+                }
+            }
+        } else {
+            const int n = l & 31;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int row = r0 + crow(r, h);
+#pragma unroll
+                for (int db = 0; db < DB; ++db) {
+                    const float a = ((const float*)(t + at(row, 8 * db + (n >> 2))))[n & 3];
+                    acc[db] = __builtin_amdgcn_mfma_f32_32x32x2f32(a, w[r], acc[db], 0, 0, 0);
+                }
+            }
+        }
+    }
+    // Writes 32 rows (lane column n = row) of D values, acc * mul, as whole rows through the wave's
+    // own 32 * CPR pieces of LDS: row n goes to out + n * stride bytes for n < rows.
+    static __device__ __forceinline__ void put_rows(const f32x16 (&acc)[DB], float mul, i32x4* buf, char* out,
+                                                    long stride, int rows) {
+        const int l = lane_id(), n = l & 31, h = l >> 5;
+#pragma unroll
+        for (int db = 0; db < DB; ++db)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const f32x4 x = {acc[db][4 * j] * mul, acc[db][4 * j + 1] * mul, acc[db][4 * j + 2] * mul, acc[db][4 * j + 3] * mul};
+                const int d0 = 32 * db + 8 * j + 4 * h, c = d0 * ES / 16;
+                if constexpr (ES == 2)
+                    *((bf16x4*)(buf + at(n, c)) + h) = bf16x4{(bf16)x[0], (bf16)x[1], (bf16)x[2], (bf16)x[3]};
+                else
+                    *(f32x4*)(buf + at(n, c)) = x;
+            }
+        wave_sync();
+#pragma unroll
+        for (int i = 0; i < 32 * CPR / 64; ++i) {
+            const int x = l + i * 64, r = x / CPR, c = x % CPR;
+            const i32x4 u = buf[at(r, c)];
+            if (r < rows) *(i32x4*)(out + r * stride + c * 16) = u;
+        }
+    }
+};
+
+// Tokens of sequence b: its length clamped to [0, T].
+__device__ __forceinline__ long swa_length(const SwaParams& p, int b) {
+    if (!p.lengths) return p.T;
+    const long L = p.lengths[b];
+    return L < 0 ? 0 : L > p.T ? p.T : L;
+}
+
+// Key tiles (of BT keys) that queries qa .. qb may see: `extra` tiles with sinks from the start of
+// the sequence, then tiles first .. last.
+struct SwaTiles {
+    int extra, first, n;
+    __device__ __forceinline__ SwaTiles(const SwaParams& p, int bt, long qa, long qb) {
+        const long lo = qa - p.window + 1;
+        first = lo > 0 ? (int)(lo / bt) : 0;
+        const int s = (p.sinks + bt - 1) / bt;
+        extra = s < first ? s : first;
+        n = extra + (int)(qb / bt) - first + 1;
+    }
+    __device__ __forceinline__ long start(int i, int bt) const { return (long)(i < extra ? i : first + i - extra) * bt; }
+};
+
+}  // namespace gdr2

@@ -1,0 +1,126 @@
+// gdr2_swa_fwd.hip -- forward of sliding-window attention with sinks (gfx950).
+//
+// Query i of a sequence of L tokens sees key j when j <= i < L and (i - j < window or j < sinks):
+//     s_ij = scale q_i . k_j,   o_i = sum_j exp(s_ij) v_j / z_i,   z_i = sum_j exp(s_ij)
+// and lse_i = ln z_i for the backward.  One pass over the keys with a running reference m_i of the
+// exponent: the terms are exp(s_ij - m_i), and m_i moves (with one rescaling of the sums) only when
+// a score exceeds it by more than 2^8, so the sums stay within fp32 and most tiles rescale nothing.
+// A workgroup takes 128 queries of one head, 32 per wave, and walks the key tiles its queries may
+// see through a double-buffered pair of LDS tiles; grouped heads share the tiles in L2.
+#include "gdr2_swa.hpp"
+
+namespace gdr2 {
+
+template <typename T, int D>
+__global__ __launch_bounds__(kSwaThreads, 2) void gdr2_swa_fwd_kernel(SwaParams p) {
+    using S = Swa<T, D>;
+    constexpr int BT = S::BT, NB = S::NB;
+    constexpr int BQ = 32 * kSwaWaves;
+    __shared__ typename S::tile lds[4];  // keys and values, two of each
+    static_assert(sizeof(lds) >= (size_t)kSwaWaves * 32 * S::CPR * 16, "output rows fit the tiles");
+    const int l = lane_id(), wv = wave_id(), n = l & 31, h = l >> 5;
+    const int nqt = (int)((p.T + BQ - 1) / BQ);
+    const int work = xcd_swizzle(blockIdx.x, gridDim.x);
+    const int qt = work % nqt, bh = work / nqt, b = bh / p.H, hd = bh % p.H, kvh = hd / (p.H / p.Hkv);
+    const long L = swa_length(p, b);
+    const long Q0 = (long)qt * BQ, q0 = Q0 + 32 * wv, i = q0 + n;
+    const long qstr = (long)p.H * D * S::ES, kstr = (long)p.Hkv * D * S::ES;
+    const char* kb = (const char*)p.k + ((long)b * p.T * p.Hkv + kvh) * D * S::ES;
+    const char* vb = (const char*)p.v + ((long)b * p.T * p.Hkv + kvh) * D * S::ES;
+    const bool live = i < L;
+    const float c = p.scale * kLog2e;
+
+    f32x16 acc[S::DB];
+#pragma unroll
+    for (int db = 0; db < S::DB; ++db) acc[db] = zero16();
+    float m = kLowest, z = 0.f;
+    if (Q0 < L) {
+        i32x4 qf[S::KK];
+        S::keep(qf, live ? (const char*)p.q + (((long)b * p.T + i) * p.H + hd) * D * S::ES : nullptr);
+        const SwaTiles tl(p, BT, Q0, Q0 + BQ <= L ? Q0 + BQ - 1 : L - 1);
+        i32x4 ku[S::UNITS], vu[S::UNITS];
+        auto fetch = [&](int t) {
+            const long j0 = tl.start(t, BT);
+            const int rows = L - j0 < BT ? (int)(L - j0) : BT;
+            S::fetch(ku, kb + j0 * kstr, kstr, rows);
+            S::fetch(vu, vb + j0 * kstr, kstr, rows);
+        };
+        fetch(0);
+        S::stage(lds[0], ku);
+        S::stage(lds[2], vu);
+        lds_barrier();
+        for (int t = 0; t < tl.n; ++t) {
+            const int cur = t & 1;
+            if (t + 1 < tl.n) fetch(t + 1);
+            const long j0 = tl.start(t, BT);
+            if (j0 <= q0 + 31 && (q0 - (j0 + BT - 1) < p.window || j0 < p.sinks)) {
+                f32x16 s[NB];
+#pragma unroll
+                for (int kb_ = 0; kb_ < NB; ++kb_) s[kb_] = S::dots(lds[cur], 32 * kb_, qf);
+                if (j0 + BT - 1 > q0 || q0 + 31 - j0 >= p.window) {
+#pragma unroll
+                    for (int kb_ = 0; kb_ < NB; ++kb_)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) {
+                            const long j = j0 + 32 * kb_ + crow(r, h);
+                            if (!(j <= i && (i - j < p.window || j < p.sinks))) s[kb_][r] = -INFINITY;
+                        }
+                }
+                float mx = s[0][0];
+#pragma unroll
+                for (int kb_ = 0; kb_ < NB; ++kb_)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[kb_][r]);
+                mx = fmaxf(mx, __shfl_xor(mx, 32)) * c;
+                if (__any(mx > m + 8.f)) {
+                    const float mn = fmaxf(m, mx), f = exp2_f(m - mn);
+                    m = mn;
+                    z *= f;
+#pragma unroll
+                    for (int db = 0; db < S::DB; ++db)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) acc[db][r] *= f;
+                }
+#pragma unroll
+                for (int kb_ = 0; kb_ < NB; ++kb_) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        s[kb_][r] = exp2_f(s[kb_][r] * c - m);
+                        z += s[kb_][r];
+                    }
+                    S::add_rows(acc, lds[2 + cur], 32 * kb_, s[kb_]);
+                }
+            }
+            if (t + 1 < tl.n) {
+                S::stage(lds[cur ^ 1], ku);
+                S::stage(lds[2 + (cur ^ 1)], vu);
+            }
+            lds_barrier();
+        }
+    }
+    z += __shfl_xor(z, 32);
+    // a query at or behind the length saw nothing: zero output, lse = -inf
+    const float inv = live ? 1.f / z : 0.f;
+    if (!live) {
+#pragma unroll
+        for (int db = 0; db < S::DB; ++db) acc[db] = zero16();
+    }
+    const int rows = p.T - q0 >= 32 ? 32 : p.T > q0 ? (int)(p.T - q0) : 0;
+    S::put_rows(acc, inv, &lds[0][0] + wv * 32 * S::CPR, (char*)p.o + (((long)b * p.T + q0) * p.H + hd) * D * S::ES,
+                qstr, rows);
+    if (h == 0 && n < rows) p.lse[(long)bh * p.T + i] = live ? (m + __builtin_amdgcn_logf(z)) * kLn2 : -INFINITY;
+}
+
+template <typename T, int D>
+static hipError_t launch_swa_fwd(const SwaParams& p, hipStream_t s) {
+    const long grid = (p.T + 127) / 128 * p.B * p.H;
+    hipLaunchKernelGGL((gdr2_swa_fwd_kernel<T, D>), dim3((unsigned)grid), dim3(kSwaThreads), 0, s, p);
+    return hipGetLastError();
+}
+
+hipError_t swa_fwd_dispatch(int bf, const SwaParams& p, hipStream_t s) {
+    if (bf) return p.d == 128 ? launch_swa_fwd<bf16, 128>(p, s) : launch_swa_fwd<bf16, 64>(p, s);
+    return p.d == 128 ? launch_swa_fwd<float, 128>(p, s) : launch_swa_fwd<float, 64>(p, s);
+}
+
+}  // namespace gdr2

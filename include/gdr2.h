@@ -374,6 +374,115 @@ gdr2_status gdr2_out_gate_bwd(int64_t rows, int64_t dv, gdr2_dtype dtype, const 
                               void* do_, void* dg, float* dweight, void* workspace,
                               size_t workspace_bytes, void* stream);
 
+/*
+ * ------------------------------------------------------------------------------------------------
+ * Operators around the mixer in a hybrid stack: the norm in front of every mixer, sliding-window
+ * attention beside the recurrent mixer (ainews.random.gg article on Gated DeltaNet-2, section "Block
+ * design and hybrid model": a 2K attention window), and an elementwise gated recurrence.  The
+ * conventions at the top of this header hold; x, q, k, v, o, y, h, their gradients and the caches
+ * have the caller's dtype, everything else is fp32.  int32 arrays (lengths, positions) live in device
+ * memory, 4-byte aligned; their values are not visible to the host checks, so every value has a
+ * meaning (below).  NaN and infinities propagate as the formulas say from the rows that are read;
+ * rows at and behind a sequence's length are not read, whatever they hold.
+ */
+
+/*
+ * Layer norm over rows of D channels (D a multiple of 8, 8 <= D <= 16384, else GDR2_E_UNSUPPORTED;
+ * rows < 2^31):
+ *     y_j = (x_j - mean) rstd weight_j + bias_j,   mean = sum_j x_j / D,
+ *     rstd = 1 / sqrt(sum_j (x_j - mean)^2 / D + eps)
+ *   x, y, dy, dx    [rows][D]  dtype
+ *   weight, bias    [D]        fp32   (bias NULL = none)
+ *   mean, rstd      [rows]     fp32   (forward outputs, NULL = not wanted; the backward reads them)
+ *   eps             > 0, finite (else GDR2_E_VALUE)
+ * The backward writes dx, dweight and dbias (NULL = not wanted), [D] fp32 sums over all rows added
+ * in a fixed order (zero for rows = 0).
+ */
+gdr2_status gdr2_layer_norm_fwd(int64_t rows, int64_t D, gdr2_dtype dtype, const void* x,
+                                const float* weight, const float* bias, float eps, void* y,
+                                float* mean, float* rstd, void* stream);
+size_t gdr2_layer_norm_bwd_workspace_bytes(int64_t rows, int64_t D);
+gdr2_status gdr2_layer_norm_bwd(int64_t rows, int64_t D, gdr2_dtype dtype, const void* x,
+                                const float* weight, const float* mean, const float* rstd,
+                                const void* dy, void* dx, float* dweight, float* dbias,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Elementwise gated linear recurrence, per batch row and channel:
+ *     h_t = exp(log_a_t) h_{t-1} + x_t,   h_0 given (NULL = zero)
+ * D a multiple of 8 (else GDR2_E_UNSUPPORTED), T >= 0 (T = 0: h_T = h_0, dh_0 = dh_T).
+ *   x, h, dh, dx    [B][T][D]  dtype
+ *   log_a, dlog_a   [B][T][D]  fp32   (natural log of the decay; any value, -inf forgets exactly)
+ *   h0, h_T         [B][D]     fp32 or NULL
+ *   workspace       gdr2_glr_fwd_workspace_bytes() bytes; on return its first part holds the state
+ *                   entering every 128-token segment, which the backward reads: keep it unchanged
+ *                   between the two calls when training
+ * The backward, for the cotangents dh of h and dh_T of h_T (NULL = zero), returns dx, dlog_a and dh0
+ * (NULL = not wanted); x, log_a as passed to the forward, fwd_workspace the forward's.  Two calls
+ * that may run at the same time need workspaces of their own.
+ * gdr2_glr_step is one token for N sequences: h_out = exp(log_a) h_in + x (fp32 state, h_in NULL =
+ * zero, h_in == h_out allowed), h the same in dtype.
+ */
+size_t gdr2_glr_fwd_workspace_bytes(int64_t B, int64_t T, int64_t D);
+gdr2_status gdr2_glr_fwd(int64_t B, int64_t T, int64_t D, gdr2_dtype dtype, const void* x,
+                         const float* log_a, const float* h0, void* h, float* h_T,
+                         void* workspace, size_t workspace_bytes, void* stream);
+size_t gdr2_glr_bwd_workspace_bytes(int64_t B, int64_t T, int64_t D);
+gdr2_status gdr2_glr_bwd(int64_t B, int64_t T, int64_t D, gdr2_dtype dtype, const void* x,
+                         const float* log_a, const void* fwd_workspace, size_t fwd_workspace_bytes,
+                         const void* dh, const float* dh_T, void* dx, float* dlog_a, float* dh0,
+                         void* workspace, size_t workspace_bytes, void* stream);
+gdr2_status gdr2_glr_step(int64_t N, int64_t D, gdr2_dtype dtype, const void* x,
+                          const float* log_a, const float* h_in, float* h_out, void* h,
+                          void* stream);
+
+/*
+ * Causal sliding-window attention whose first `sinks` tokens stay visible.  Query i of a sequence of
+ * L tokens sees key j when j <= i < L and (i - j < window or j < sinks):
+ *     o_i = sum_j softmax_j(scale q_i . k_j) v_j,   lse_i = log sum_j exp(scale q_i . k_j)
+ * Query head h reads key/value head h / (H / Hkv); H must be a multiple of Hkv (else GDR2_E_SHAPE).
+ *   q, o, dO, dq    [B][T][H][d]    dtype       d in {64, 128}
+ *   k, v, dk, dv    [B][T][Hkv][d]  dtype
+ *   lengths         [B] int32 or NULL (every sequence has T tokens); values are clamped to [0, T].
+ *                   Rows at and behind the length are padding: o, dq, dk, dv are zero there, lse -inf
+ *   lse             [B][H][T] fp32 (natural log)
+ *   window          >= 1;  0 <= sinks <= 64;  scale > 0, finite (else GDR2_E_VALUE)
+ * The backward takes the forward's o and lse.  dk and dv are summed over the heads that share them.
+ */
+gdr2_status gdr2_swa_fwd(int64_t B, int64_t T, int64_t H, int64_t Hkv, int64_t d, gdr2_dtype dtype,
+                         int64_t window, int64_t sinks, float scale, const void* q, const void* k,
+                         const void* v, const int32_t* lengths, void* o, float* lse, void* stream);
+size_t gdr2_swa_bwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Hkv, int64_t d,
+                                    int64_t window, int64_t sinks);
+gdr2_status gdr2_swa_bwd(int64_t B, int64_t T, int64_t H, int64_t Hkv, int64_t d, gdr2_dtype dtype,
+                         int64_t window, int64_t sinks, float scale, const void* q, const void* k,
+                         const void* v, const int32_t* lengths, const void* o, const float* lse,
+                         const void* dO, void* dq, void* dk, void* dv, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/*
+ * The bounded cache of that attention for decoding: [N][sinks + window][Hkv][d] per keys and values.
+ * Position p lives in slot p (p < sinks) or sinks + (p - sinks) mod window, so a sequence of any
+ * length needs window + sinks rows.
+ * gdr2_swa_cache_fill stores, from a prefill's k and v ([B][T][Hkv][d]), the positions a token at
+ * position L (the length) may still see into their slots; other slots are left as they were.
+ * gdr2_swa_decode_step stores the new token's k and v ([N][Hkv][d]) at position pos[n] into the cache
+ * and returns its attention output o ([N][H][d]) over the positions the window and the sinks leave
+ * visible; the cache must hold positions 0 .. pos[n] - 1 as far as they fit.  A negative pos[n]
+ * means that sequence has no token: o is zero, its cache stays.  Slots not written yet are not used.
+ *   workspace       gdr2_swa_decode_workspace_bytes() bytes (0: none needed)
+ */
+gdr2_status gdr2_swa_cache_fill(int64_t B, int64_t T, int64_t Hkv, int64_t d, gdr2_dtype dtype,
+                                int64_t window, int64_t sinks, const void* k, const void* v,
+                                const int32_t* lengths, void* k_cache, void* v_cache, void* stream);
+size_t gdr2_swa_decode_workspace_bytes(int64_t N, int64_t H, int64_t Hkv, int64_t d,
+                                       int64_t window, int64_t sinks);
+gdr2_status gdr2_swa_decode_step(int64_t N, int64_t H, int64_t Hkv, int64_t d, gdr2_dtype dtype,
+                                 int64_t window, int64_t sinks, float scale, const void* q,
+                                 const void* k, const void* v, void* k_cache, void* v_cache,
+                                 const int32_t* pos, void* o, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* gdr2_status_string(gdr2_status s);
 
