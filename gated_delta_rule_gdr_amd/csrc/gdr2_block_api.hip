@@ -79,7 +79,7 @@ gdr2::SwaParams swa_params(int64_t B, int64_t T, int64_t H, int64_t Hkv, int64_t
                            float scale, const void* q, const void* k, const void* v, const int32_t* lengths) {
     gdr2::SwaParams p{};
     p.B = (int)B; p.H = (int)H; p.Hkv = (int)Hkv; p.d = (int)d; p.sinks = (int)sinks;
-    p.T = T; p.window = window < T ? window : T;
+    p.T = (int)T; p.window = (int)(window < T ? window : T);
     p.scale = scale; p.q = q; p.k = k; p.v = v; p.lengths = lengths;
     return p;
 }
@@ -284,7 +284,7 @@ gdr2_status gdr2_swa_bwd(int64_t B, int64_t T, int64_t H, int64_t Hkv, int64_t d
     p.o = (void*)o; p.lse = (float*)lse; p.dO = dO; p.dq = dq; p.dk = dk; p.dv = dv;
     p.delta = (float*)((char*)workspace + w.delta);
     p.sink_part = (float*)((char*)workspace + w.part);
-    p.pieces = w.far.pieces; p.far0 = w.far.far0; p.piece_len = w.far.piece_len;
+    p.pieces = w.far.pieces; p.far0 = (int)w.far.far0; p.piece_len = (int)w.far.piece_len;
     return status_of(gdr2::swa_bwd_dispatch(dt == GDR2_BF16, p, (hipStream_t)stream));
 }
 

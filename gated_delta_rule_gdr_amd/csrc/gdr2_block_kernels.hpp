@@ -66,7 +66,7 @@ constexpr int kSwaKeyTile = 128;    // keys of a key/value-gradient workgroup
 constexpr int kSwaSinkPieces = 16;  // at most this many pieces of the queries behind the window
 struct SwaParams {
     int B, H, Hkv, d, sinks;
-    long T, window;         // window <= T
+    int T, window;          // T <= 2^30, window <= T
     float scale;
     const void *q, *k, *v;  // [B][T][H][d], [B][T][Hkv][d]
     const int* lengths;     // [B] or null (every sequence has T tokens)
@@ -77,7 +77,7 @@ struct SwaParams {
     float* delta;           // [B][H][T] sum of dO o per query (backward workspace)
     float* sink_part;       // [pieces][B][Hkv][2][64][d] dk, dv of the sinks from far queries
     int pieces;             // 0: no query lies behind the window, or no sinks
-    long far0, piece_len;   // piece i covers queries far0 + i * piece_len ..
+    int far0, piece_len;    // piece i covers queries far0 + i * piece_len ..
 };
 // Pieces of the far queries (those the first key tile's workgroup does not walk) for sinks > 0.
 struct SwaFar {

@@ -56,11 +56,10 @@ struct Swa {
         }
     }
     static __device__ __forceinline__ void stage(i32x4* t, const i32x4 (&u)[UNITS]) {
+        constexpr int RSTEP = kSwaThreads / CPR;  // rows between a thread's pieces
+        const int r0 = threadIdx.x / CPR, c = threadIdx.x % CPR, p0 = at(r0, c);
 #pragma unroll
-        for (int i = 0; i < UNITS; ++i) {
-            const int x = threadIdx.x + i * kSwaThreads;
-            t[at(x / CPR, x % CPR)] = u[i];
-        }
+        for (int i = 0; i < UNITS; ++i) t[RSTEP % 16 ? at(r0 + i * RSTEP, c) : p0 + i * kSwaThreads] = u[i];
     }
     // the B operand of 32 rows, kept in registers: piece 2 kk + h of the lane's row (null: zeros)
     static __device__ __forceinline__ void keep(i32x4 (&f)[KK], const char* row) {
@@ -146,25 +145,42 @@ struct Swa {
     }
 };
 
+// the wave's index as a wave-uniform value, so that conditions on its rows are scalar branches
+__device__ __forceinline__ int uniform_wave() { return __builtin_amdgcn_readfirstlane(wave_id()); }
+
+// Positions inside a sequence are ints (T <= 2^30); addresses are formed in 64 bits.
 // Tokens of sequence b: its length clamped to [0, T].
-__device__ __forceinline__ long swa_length(const SwaParams& p, int b) {
+__device__ __forceinline__ int swa_length(const SwaParams& p, int b) {
     if (!p.lengths) return p.T;
-    const long L = p.lengths[b];
+    const int L = p.lengths[b];
     return L < 0 ? 0 : L > p.T ? p.T : L;
+}
+// Keeps the masking of an edge tile behind its branch: most tiles are seen whole.
+__device__ __forceinline__ void edge_tile() { asm volatile(""); }
+// Calls f(t, IC<buffer>) for t = 0 .. n - 1 with the LDS buffer t % 2 as a constant.
+template <typename F>
+__device__ __forceinline__ void for_tiles(int n, F&& f) {
+    for (int t = 0; t < n; t += 2) {
+        f(t, IC<0>{});
+        if (t + 1 < n) f(t + 1, IC<1>{});
+    }
+}
+__device__ __forceinline__ bool swa_sees(const SwaParams& p, int i, int j) {
+    return j <= i && (i - j < p.window || j < p.sinks);
 }
 
 // Key tiles (of BT keys) that queries qa .. qb may see: `extra` tiles with sinks from the start of
 // the sequence, then tiles first .. last.
 struct SwaTiles {
     int extra, first, n;
-    __device__ __forceinline__ SwaTiles(const SwaParams& p, int bt, long qa, long qb) {
-        const long lo = qa - p.window + 1;
-        first = lo > 0 ? (int)(lo / bt) : 0;
+    __device__ __forceinline__ SwaTiles(const SwaParams& p, int bt, int qa, int qb) {
+        const int lo = qa - p.window + 1;
+        first = lo > 0 ? lo / bt : 0;
         const int s = (p.sinks + bt - 1) / bt;
         extra = s < first ? s : first;
-        n = extra + (int)(qb / bt) - first + 1;
+        n = extra + qb / bt - first + 1;
     }
-    __device__ __forceinline__ long start(int i, int bt) const { return (long)(i < extra ? i : first + i - extra) * bt; }
+    __device__ __forceinline__ int start(int i, int bt) const { return (i < extra ? i : first + i - extra) * bt; }
 };
 
 }  // namespace gdr2

@@ -24,12 +24,12 @@ __global__ __launch_bounds__(kSwaThreads, sizeof(T) * D > 256 ? 1 : 2) void gdr2
     constexpr int BT = S::BT, NB = S::NB;
     constexpr int BQ = 32 * kSwaWaves;
     __shared__ typename S::tile lds[4];
-    const int l = lane_id(), wv = wave_id(), n = l & 31, h = l >> 5;
+    const int l = lane_id(), wv = uniform_wave(), n = l & 31, h = l >> 5;
     const int nqt = (int)((p.T + BQ - 1) / BQ);
     const int work = xcd_swizzle(blockIdx.x, gridDim.x);
     const int qt = work % nqt, bh = work / nqt, b = bh / p.H, hd = bh % p.H, kvh = hd / (p.H / p.Hkv);
-    const long L = swa_length(p, b);
-    const long Q0 = (long)qt * BQ, q0 = Q0 + 32 * wv, i = q0 + n;
+    const int L = swa_length(p, b);
+    const int Q0 = qt * BQ, q0 = Q0 + 32 * wv, i = q0 + n;
     const long qstr = (long)p.H * D * S::ES, kstr = (long)p.Hkv * D * S::ES;
     const char* kb = (const char*)p.k + ((long)b * p.T * p.Hkv + kvh) * D * S::ES;
     const char* vb = (const char*)p.v + ((long)b * p.T * p.Hkv + kvh) * D * S::ES;
@@ -66,8 +66,8 @@ __global__ __launch_bounds__(kSwaThreads, sizeof(T) * D > 256 ? 1 : 2) void gdr2
         const SwaTiles tl(p, BT, Q0, Q0 + BQ <= L ? Q0 + BQ - 1 : L - 1);
         i32x4 ku[S::UNITS], vu[S::UNITS];
         auto fetch = [&](int t) {
-            const long j0 = tl.start(t, BT);
-            const int rows = L - j0 < BT ? (int)(L - j0) : BT;
+            const int j0 = tl.start(t, BT);
+            const int rows = L - j0 < BT ? L - j0 : BT;
             S::fetch(ku, kb + j0 * kstr, kstr, rows);
             S::fetch(vu, vb + j0 * kstr, kstr, rows);
         };
@@ -75,10 +75,10 @@ __global__ __launch_bounds__(kSwaThreads, sizeof(T) * D > 256 ? 1 : 2) void gdr2
         S::stage(lds[0], ku);
         S::stage(lds[2], vu);
         lds_barrier();
-        for (int t = 0; t < tl.n; ++t) {
-            const int cur = t & 1;
+        for_tiles(tl.n, [&](int t, auto buf_) {
+            constexpr int cur = decltype(buf_)::value;
             if (t + 1 < tl.n) fetch(t + 1);
-            const long j0 = tl.start(t, BT);
+            const int j0 = tl.start(t, BT);
             if (j0 <= q0 + 31 && (q0 - (j0 + BT - 1) < p.window || j0 < p.sinks)) {
                 const bool edge = j0 + BT - 1 > q0 || q0 + 31 - j0 >= p.window;
 #pragma unroll
@@ -86,11 +86,10 @@ __global__ __launch_bounds__(kSwaThreads, sizeof(T) * D > 256 ? 1 : 2) void gdr2
                     f32x16 s = S::dots(lds[cur], 32 * k_, qf);
                     const f32x16 dp = S::dots(lds[2 + cur], 32 * k_, gf);
                     if (edge) {
+                        edge_tile();
 #pragma unroll
-                        for (int r = 0; r < 16; ++r) {
-                            const long j = j0 + 32 * k_ + crow(r, h);
-                            if (!(j <= i && (i - j < p.window || j < p.sinks))) s[r] = -INFINITY;
-                        }
+                        for (int r = 0; r < 16; ++r)
+                            if (!swa_sees(p, i, j0 + 32 * k_ + crow(r, h))) s[r] = -INFINITY;
                     }
 #pragma unroll
                     for (int r = 0; r < 16; ++r) s[r] = exp2_f(s[r] * c - lse2) * (dp[r] - delta);
@@ -102,9 +101,9 @@ __global__ __launch_bounds__(kSwaThreads, sizeof(T) * D > 256 ? 1 : 2) void gdr2
                 S::stage(lds[2 + (cur ^ 1)], vu);
             }
             lds_barrier();
-        }
+        });
     }
-    const int rows = p.T - q0 >= 32 ? 32 : p.T > q0 ? (int)(p.T - q0) : 0;
+    const int rows = p.T - q0 >= 32 ? 32 : p.T > q0 ? p.T - q0 : 0;
     S::put_rows(acc, p.scale, &lds[0][0] + wv * 32 * S::CPR,
                 (char*)p.dq + (((long)b * p.T + q0) * p.H + hd) * D * S::ES, qstr, rows);
     if (h == 0 && n < rows) p.delta[(long)bh * p.T + i] = delta;
@@ -124,16 +123,15 @@ struct SwaKeys {
         for (int db = 0; db < S::DB; ++db) dk[db] = dv[db] = zero16();
     }
     __device__ __forceinline__ void step(const SwaParams& p, const i32x4* qt, const i32x4* gt, const float* ls, const float* dl,
-                                         int r0, long i0, long j, bool edge, float c) {
+                                         int r0, int i0, int j, bool edge, float c) {
         const int h = lane_id() >> 5;
         f32x16 s = S::dots(qt, r0, kf);
         f32x16 dp = S::dots(gt, r0, vf);
-        if (edge) {
+        if (edge) {  // some pairs of the block are hidden
+            edge_tile();
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const long i = i0 + r0 + crow(r, h);
-                if (!(j <= i && (i - j < p.window || j < p.sinks))) s[r] = -INFINITY;
-            }
+            for (int r = 0; r < 16; ++r)
+                if (!swa_sees(p, i0 + r0 + crow(r, h), j)) s[r] = -INFINITY;
         }
 #pragma unroll
         for (int r4 = 0; r4 < 4; ++r4) {
@@ -156,9 +154,9 @@ struct SwaQueries {
     i32x4 qu[S::UNITS], gu[S::UNITS];
     float su;
     // threads 0 .. BT - 1: lse, BT .. 2 BT - 1: delta of the tile's rows
-    __device__ __forceinline__ void fetch(const SwaParams& p, int b, int hd, long i0, long L) {
+    __device__ __forceinline__ void fetch(const SwaParams& p, int b, int hd, int i0, int L) {
         const long qstr = (long)p.H * D * S::ES, off = (((long)b * p.T + i0) * p.H + hd) * D * S::ES;
-        const int rows = L - i0 < S::BT ? (int)(L - i0) : S::BT;
+        const int rows = L - i0 < S::BT ? L - i0 : S::BT;
         S::fetch(qu, (const char*)p.q + off, qstr, rows);
         S::fetch(gu, (const char*)p.dO + off, qstr, rows);
         const int x = threadIdx.x, r = x % S::BT;
@@ -181,12 +179,12 @@ __global__ __launch_bounds__(kSwaThreads, sizeof(T) * D > 128 ? 1 : 2) void gdr2
     static_assert(kSwaKeyTile == 32 * kSwaWaves, "a wave holds 32 keys");
     __shared__ typename S::tile lds[4];  // queries and cotangents, two of each
     __shared__ float sc[2][2 * BT];
-    const int l = lane_id(), wv = wave_id(), n = l & 31, h = l >> 5;
+    const int l = lane_id(), wv = uniform_wave(), n = l & 31, h = l >> 5;
     const int nkt = (int)((p.T + kSwaKeyTile - 1) / kSwaKeyTile);
     const int work = xcd_swizzle(blockIdx.x, gridDim.x);
     const int kt = work % nkt, bh = work / nkt, b = bh / p.Hkv, kvh = bh % p.Hkv, G = p.H / p.Hkv;
-    const long L = swa_length(p, b);
-    const long K0 = (long)kt * kSwaKeyTile, k0 = K0 + 32 * wv, j = k0 + n;
+    const int L = swa_length(p, b);
+    const int K0 = kt * kSwaKeyTile, k0 = K0 + 32 * wv, j = k0 + n;
     const long kstr = (long)p.Hkv * D * S::ES;
     const long koff = (((long)b * p.T + j) * p.Hkv + kvh) * D * S::ES;
     const float c = p.scale * kLog2e;
@@ -194,28 +192,28 @@ __global__ __launch_bounds__(kSwaThreads, sizeof(T) * D > 128 ? 1 : 2) void gdr2
     ks.init(j < L ? (const char*)p.k + koff : nullptr, j < L ? (const char*)p.v + koff : nullptr);
     if (K0 < L) {
         // the queries that see the tile's last key; with sinks, the first tile's go on to the far ones
-        const long seen = kt == 0 && p.sinks > 0 ? p.far0 : K0 + kSwaKeyTile - 1 + p.window;
-        const long i_end = seen < L ? seen : L;
-        const int t0 = (int)(K0 / BT), per = (int)((i_end + BT - 1) / BT) - t0, nt = per * G;
+        const int seen = kt == 0 && p.sinks > 0 ? p.far0 : K0 + kSwaKeyTile - 1 + p.window;
+        const int i_end = seen < L ? seen : L;
+        const int t0 = K0 / BT, per = (i_end + BT - 1) / BT - t0, nt = per * G;
         SwaQueries<T, D> qs;
-        auto fetch = [&](int t) { qs.fetch(p, b, kvh * G + t / per, (long)(t0 + t % per) * BT, L); };
+        auto fetch = [&](int t) { qs.fetch(p, b, kvh * G + t / per, (t0 + t % per) * BT, L); };
         fetch(0);
         qs.stage(lds[0], lds[2], sc[0]);
         lds_barrier();
-        for (int t = 0; t < nt; ++t) {
-            const int cur = t & 1;
+        for_tiles(nt, [&](int t, auto buf_) {
+            constexpr int cur = decltype(buf_)::value;
             if (t + 1 < nt) fetch(t + 1);
-            const long i0 = (long)(t0 + t % per) * BT;
+            const int i0 = (t0 + t % per) * BT;
 #pragma unroll
             for (int r = 0; r < NB; ++r) {
-                const long ia = i0 + 32 * r;
+                const int ia = i0 + 32 * r;
                 if (ia + 31 >= k0 && (ia - (k0 + 31) < p.window || k0 < p.sinks))
                     ks.step(p, lds[cur], lds[2 + cur], sc[cur], sc[cur] + BT, 32 * r, i0, j,
                             ia < k0 + 31 || ia + 31 - k0 >= p.window, c);
             }
             if (t + 1 < nt) qs.stage(lds[cur ^ 1], lds[2 + (cur ^ 1)], sc[cur ^ 1]);
             lds_barrier();
-        }
+        });
     }
     // the sinks' sums over the far queries, piece by piece
     if (kt == 0 && p.pieces > 0 && k0 < p.sinks) {
@@ -236,7 +234,7 @@ __global__ __launch_bounds__(kSwaThreads, sizeof(T) * D > 128 ? 1 : 2) void gdr2
                 }
         }
     }
-    const int rows = p.T - k0 >= 32 ? 32 : p.T > k0 ? (int)(p.T - k0) : 0;
+    const int rows = p.T - k0 >= 32 ? 32 : p.T > k0 ? p.T - k0 : 0;
     const long ooff = (((long)b * p.T + k0) * p.Hkv + kvh) * D * S::ES;
     i32x4* buf = &lds[0][0] + wv * 32 * S::CPR;
     S::put_rows(ks.dk, p.scale, buf, (char*)p.dk + ooff, kstr, rows);
@@ -253,14 +251,14 @@ __global__ __launch_bounds__(kSwaThreads, sizeof(T) * D > 128 ? 1 : 2) void gdr2
     __shared__ typename S::tile lds[4];
     __shared__ float sc[2][2 * BT];
     static_assert(sizeof(lds) >= 2 * 32 * D * 2 * sizeof(float), "partial sums of two waves fit the tiles");
-    const int l = lane_id(), wv = wave_id(), n = l & 31, h = l >> 5;
+    const int l = lane_id(), wv = uniform_wave(), n = l & 31, h = l >> 5;
     const int piece = blockIdx.x % p.pieces, bh = blockIdx.x / p.pieces, b = bh / p.Hkv, kvh = bh % p.Hkv, G = p.H / p.Hkv;
-    const long L = swa_length(p, b);
-    const long ia = p.far0 + piece * p.piece_len;
+    const int L = swa_length(p, b);
+    const int ia = p.far0 + piece * p.piece_len;
     if (ia >= L) return;  // the first key tile skips this piece too
-    const long ib = ia + p.piece_len < L ? ia + p.piece_len : L;
+    const int ib = ia + p.piece_len < L ? ia + p.piece_len : L;
     const int rb = wv % NB, key0 = 32 * (wv / NB);
-    const long j = key0 + n;
+    const int j = key0 + n;
     const bool mine = key0 < p.sinks;
     const float c = p.scale * kLog2e;
     const long koff = (((long)b * p.T + j) * p.Hkv + kvh) * D * S::ES;
@@ -268,19 +266,19 @@ __global__ __launch_bounds__(kSwaThreads, sizeof(T) * D > 128 ? 1 : 2) void gdr2
     const bool key = j < p.sinks && j < L;
     SwaKeys<T, D> ks;
     ks.init(key ? (const char*)p.k + koff : nullptr, key ? (const char*)p.v + koff : nullptr);
-    const int per = (int)((ib - ia + BT - 1) / BT), nt = per * G;
+    const int per = (ib - ia + BT - 1) / BT, nt = per * G;
     SwaQueries<T, D> qs;
-    auto fetch = [&](int t) { qs.fetch(p, b, kvh * G + t / per, ia + (long)(t % per) * BT, L); };
+    auto fetch = [&](int t) { qs.fetch(p, b, kvh * G + t / per, ia + t % per * BT, L); };
     fetch(0);
     qs.stage(lds[0], lds[2], sc[0]);
     lds_barrier();
-    for (int t = 0; t < nt; ++t) {
-        const int cur = t & 1;
+    for_tiles(nt, [&](int t, auto buf_) {
+        constexpr int cur = decltype(buf_)::value;
         if (t + 1 < nt) fetch(t + 1);
-        if (mine) ks.step(p, lds[cur], lds[2 + cur], sc[cur], sc[cur] + BT, 32 * rb, ia + (long)(t % per) * BT, j, true, c);
+        if (mine) ks.step(p, lds[cur], lds[2 + cur], sc[cur], sc[cur] + BT, 32 * rb, ia + t % per * BT, j, true, c);
         if (t + 1 < nt) qs.stage(lds[cur ^ 1], lds[2 + (cur ^ 1)], sc[cur ^ 1]);
         lds_barrier();
-    }
+    });
     // two query blocks of one key block: the second wave's sums through LDS
     float* buf = (float*)&lds[0][0] + (wv / NB) * 2 * 32 * D;
     auto place = [&](int db, int r4) { return n * D + 32 * db + 8 * r4 + 4 * h; };
@@ -317,7 +315,7 @@ __global__ __launch_bounds__(kSwaThreads, sizeof(T) * D > 128 ? 1 : 2) void gdr2
 
 template <typename T, int D>
 static hipError_t launch_swa_bwd(const SwaParams& p, hipStream_t s) {
-    const long gq = (p.T + 127) / 128 * p.B * p.H, gk = (p.T + kSwaKeyTile - 1) / kSwaKeyTile * p.B * p.Hkv;
+    const long gq = (long)((p.T + 127) / 128) * p.B * p.H, gk = (long)((p.T + kSwaKeyTile - 1) / kSwaKeyTile) * p.B * p.Hkv;
     hipLaunchKernelGGL((gdr2_swa_dq_kernel<T, D>), dim3((unsigned)gq), dim3(kSwaThreads), 0, s, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

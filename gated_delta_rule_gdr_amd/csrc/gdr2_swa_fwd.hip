@@ -18,12 +18,12 @@ __global__ __launch_bounds__(kSwaThreads, 2) void gdr2_swa_fwd_kernel(SwaParams 
     constexpr int BQ = 32 * kSwaWaves;
     __shared__ typename S::tile lds[4];  // keys and values, two of each
     static_assert(sizeof(lds) >= (size_t)kSwaWaves * 32 * S::CPR * 16, "output rows fit the tiles");
-    const int l = lane_id(), wv = wave_id(), n = l & 31, h = l >> 5;
+    const int l = lane_id(), wv = uniform_wave(), n = l & 31, h = l >> 5;
     const int nqt = (int)((p.T + BQ - 1) / BQ);
     const int work = xcd_swizzle(blockIdx.x, gridDim.x);
     const int qt = work % nqt, bh = work / nqt, b = bh / p.H, hd = bh % p.H, kvh = hd / (p.H / p.Hkv);
-    const long L = swa_length(p, b);
-    const long Q0 = (long)qt * BQ, q0 = Q0 + 32 * wv, i = q0 + n;
+    const int L = swa_length(p, b);
+    const int Q0 = qt * BQ, q0 = Q0 + 32 * wv, i = q0 + n;
     const long qstr = (long)p.H * D * S::ES, kstr = (long)p.Hkv * D * S::ES;
     const char* kb = (const char*)p.k + ((long)b * p.T * p.Hkv + kvh) * D * S::ES;
     const char* vb = (const char*)p.v + ((long)b * p.T * p.Hkv + kvh) * D * S::ES;
@@ -40,8 +40,8 @@ __global__ __launch_bounds__(kSwaThreads, 2) void gdr2_swa_fwd_kernel(SwaParams 
         const SwaTiles tl(p, BT, Q0, Q0 + BQ <= L ? Q0 + BQ - 1 : L - 1);
         i32x4 ku[S::UNITS], vu[S::UNITS];
         auto fetch = [&](int t) {
-            const long j0 = tl.start(t, BT);
-            const int rows = L - j0 < BT ? (int)(L - j0) : BT;
+            const int j0 = tl.start(t, BT);
+            const int rows = L - j0 < BT ? L - j0 : BT;
             S::fetch(ku, kb + j0 * kstr, kstr, rows);
             S::fetch(vu, vb + j0 * kstr, kstr, rows);
         };
@@ -49,21 +49,21 @@ __global__ __launch_bounds__(kSwaThreads, 2) void gdr2_swa_fwd_kernel(SwaParams 
         S::stage(lds[0], ku);
         S::stage(lds[2], vu);
         lds_barrier();
-        for (int t = 0; t < tl.n; ++t) {
-            const int cur = t & 1;
+        for_tiles(tl.n, [&](int t, auto buf_) {
+            constexpr int cur = decltype(buf_)::value;
             if (t + 1 < tl.n) fetch(t + 1);
-            const long j0 = tl.start(t, BT);
+            const int j0 = tl.start(t, BT);
             if (j0 <= q0 + 31 && (q0 - (j0 + BT - 1) < p.window || j0 < p.sinks)) {
                 f32x16 s[NB];
 #pragma unroll
                 for (int kb_ = 0; kb_ < NB; ++kb_) s[kb_] = S::dots(lds[cur], 32 * kb_, qf);
                 if (j0 + BT - 1 > q0 || q0 + 31 - j0 >= p.window) {
+                    edge_tile();
 #pragma unroll
                     for (int kb_ = 0; kb_ < NB; ++kb_)
 #pragma unroll
                         for (int r = 0; r < 16; ++r) {
-                            const long j = j0 + 32 * kb_ + crow(r, h);
-                            if (!(j <= i && (i - j < p.window || j < p.sinks))) s[kb_][r] = -INFINITY;
+                            if (!swa_sees(p, i, j0 + 32 * kb_ + crow(r, h))) s[kb_][r] = -INFINITY;
                         }
                 }
                 float mx = s[0][0];
@@ -71,9 +71,8 @@ __global__ __launch_bounds__(kSwaThreads, 2) void gdr2_swa_fwd_kernel(SwaParams 
                 for (int kb_ = 0; kb_ < NB; ++kb_)
 #pragma unroll
                     for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[kb_][r]);
-                mx = fmaxf(mx, __shfl_xor(mx, 32)) * c;
-                if (__any(mx > m + 8.f)) {
-                    const float mn = fmaxf(m, mx), f = exp2_f(m - mn);
+                if (__any(mx * c > m + 8.f)) {  // rare once the reference has settled
+                    const float mn = fmaxf(m, fmaxf(mx, __shfl_xor(mx, 32)) * c), f = exp2_f(m - mn);
                     m = mn;
                     z *= f;
 #pragma unroll
@@ -96,7 +95,7 @@ __global__ __launch_bounds__(kSwaThreads, 2) void gdr2_swa_fwd_kernel(SwaParams 
                 S::stage(lds[2 + (cur ^ 1)], vu);
             }
             lds_barrier();
-        }
+        });
     }
     z += __shfl_xor(z, 32);
     // a query at or behind the length saw nothing: zero output, lse = -inf
@@ -105,7 +104,7 @@ __global__ __launch_bounds__(kSwaThreads, 2) void gdr2_swa_fwd_kernel(SwaParams 
 #pragma unroll
         for (int db = 0; db < S::DB; ++db) acc[db] = zero16();
     }
-    const int rows = p.T - q0 >= 32 ? 32 : p.T > q0 ? (int)(p.T - q0) : 0;
+    const int rows = p.T - q0 >= 32 ? 32 : p.T > q0 ? p.T - q0 : 0;
     S::put_rows(acc, inv, &lds[0][0] + wv * 32 * S::CPR, (char*)p.o + (((long)b * p.T + q0) * p.H + hd) * D * S::ES,
                 qstr, rows);
     if (h == 0 && n < rows) p.lse[(long)bh * p.T + i] = live ? (m + __builtin_amdgcn_logf(z)) * kLn2 : -INFINITY;
@@ -113,7 +112,7 @@ __global__ __launch_bounds__(kSwaThreads, 2) void gdr2_swa_fwd_kernel(SwaParams 
 
 template <typename T, int D>
 static hipError_t launch_swa_fwd(const SwaParams& p, hipStream_t s) {
-    const long grid = (p.T + 127) / 128 * p.B * p.H;
+    const long grid = (long)((p.T + 127) / 128) * p.B * p.H;
     hipLaunchKernelGGL((gdr2_swa_fwd_kernel<T, D>), dim3((unsigned)grid), dim3(kSwaThreads), 0, s, p);
     return hipGetLastError();
 }
