@@ -59,7 +59,7 @@ GlrWs glr_layout(int64_t B, int64_t T, int64_t D, bool with_states) {
 
 // ------------------------------------------------------------------ sliding-window attention
 gdr2_status check_heads(int64_t H, int64_t Hkv, int64_t d, int64_t window, int64_t sinks) {
-    if (H < 0 || Hkv < 0 || d < 0 || H > ((int64_t)1 << 24)) return GDR2_E_SHAPE;
+    if (H < 0 || Hkv < 0 || d < 0 || H > 32768) return GDR2_E_SHAPE;  // a token's row stays below 2^24 + 1 bytes
     if (!dims_ok(d)) return GDR2_E_UNSUPPORTED;
     if (H > 0 && (Hkv == 0 || H % Hkv)) return GDR2_E_SHAPE;
     if (H == 0 && Hkv != 0) return GDR2_E_SHAPE;
@@ -72,7 +72,7 @@ gdr2_status check_swa(int64_t B, int64_t T, int64_t H, int64_t Hkv, int64_t d, i
     const gdr2_status st = check_heads(H, Hkv, d, window, sinks);
     if (st != GDR2_OK) return st;
     if (B < 0 || T < 0 || T > ((int64_t)1 << 30)) return GDR2_E_SHAPE;
-    if (!prod_le(B, H, kMaxGrid) || !prod_le(B * H, (T + 127) / 128 + gdr2::kSwaSinkPieces, kMaxGrid)) return GDR2_E_SHAPE;
+    if (!prod_le(B, H, kMaxGrid) || !prod_le(B * H, (T + 63) / 64 + 64, kMaxGrid / 8)) return GDR2_E_SHAPE;
     return GDR2_OK;
 }
 gdr2::SwaParams swa_params(int64_t B, int64_t T, int64_t H, int64_t Hkv, int64_t d, int64_t window, int64_t sinks,
@@ -84,15 +84,19 @@ gdr2::SwaParams swa_params(int64_t B, int64_t T, int64_t H, int64_t Hkv, int64_t
     return p;
 }
 struct SwaBwdWs {
-    size_t delta, part, total;
-    gdr2::SwaFar far;
+    size_t delta, sinks, keys, total;
+    gdr2::SwaCut cut;
 };
 SwaBwdWs swa_bwd_layout(int64_t B, int64_t T, int64_t H, int64_t Hkv, int64_t d, int64_t window, int64_t sinks) {
     SwaBwdWs w{};
-    w.far = gdr2::swa_far(T, window < T ? window : T, (int)sinks);
-    w.delta = 0;
-    w.part = round_up((size_t)B * H * T * 4, 256);
-    w.total = w.part + round_up((size_t)w.far.pieces * B * Hkv * 2 * gdr2::kSwaMaxSinks * d * 4, 256);
+    if (B == 0 || T == 0 || H == 0) return w;
+    w.cut = gdr2::swa_cut(B, T, H, Hkv, window < T ? window : T, (int)sinks);
+    size_t off = 0;
+    auto take = [&](size_t n) { const size_t o = off; off += round_up(n, 256); return o; };
+    w.delta = take((size_t)B * H * T * 4);
+    w.sinks = take((size_t)w.cut.pieces * B * Hkv * 2 * gdr2::kSwaMaxSinks * d * 4);
+    w.keys = take((size_t)w.cut.splits * 2 * B * w.cut.part_rows * Hkv * d * 4);
+    w.total = off;
     return w;
 }
 gdr2_status check_decode(int64_t N, int64_t H, int64_t Hkv, int64_t d, int64_t window, int64_t sinks) {
@@ -283,8 +287,10 @@ gdr2_status gdr2_swa_bwd(int64_t B, int64_t T, int64_t H, int64_t Hkv, int64_t d
     gdr2::SwaParams p = swa_params(B, T, H, Hkv, d, window, sinks, scale, q, k, v, lengths);
     p.o = (void*)o; p.lse = (float*)lse; p.dO = dO; p.dq = dq; p.dk = dk; p.dv = dv;
     p.delta = (float*)((char*)workspace + w.delta);
-    p.sink_part = (float*)((char*)workspace + w.part);
-    p.pieces = w.far.pieces; p.far0 = (int)w.far.far0; p.piece_len = (int)w.far.piece_len;
+    p.sink_part = (float*)((char*)workspace + w.sinks);
+    p.key_part = (float*)((char*)workspace + w.keys);
+    p.splits = w.cut.splits; p.part_rows = w.cut.part_rows; p.pieces = w.cut.pieces;
+    p.far0 = w.cut.far0; p.piece_len = w.cut.piece_len;
     return status_of(gdr2::swa_bwd_dispatch(dt == GDR2_BF16, p, (hipStream_t)stream));
 }
 

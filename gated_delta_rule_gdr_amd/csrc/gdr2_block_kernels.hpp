@@ -63,7 +63,6 @@ hipError_t glr_step_dispatch(int dtype_bf16, const GlrStepParams& p, hipStream_t
 // j <= i < L and (i - j < window or j < sinks).
 constexpr int kSwaMaxSinks = 64;
 constexpr int kSwaKeyTile = 128;    // keys of a key/value-gradient workgroup
-constexpr int kSwaSinkPieces = 16;  // at most this many pieces of the queries behind the window
 struct SwaParams {
     int B, H, Hkv, d, sinks;
     int T, window;          // T <= 2^30, window <= T
@@ -75,21 +74,40 @@ struct SwaParams {
     const void* dO;         // backward
     void *dq, *dk, *dv;
     float* delta;           // [B][H][T] sum of dO o per query (backward workspace)
-    float* sink_part;       // [pieces][B][Hkv][2][64][d] dk, dv of the sinks from far queries
+    // dk and dv in parts (backward workspace, fp32)
+    float* sink_part;       // [pieces][B][Hkv][2][64][d]: the sinks' from the far queries
+    float* key_part;        // [splits][2][B][part_rows][Hkv][d]
+    int splits, part_rows;  // part_rows: rows that the reduction writes (0: it is not needed)
     int pieces;             // 0: no query lies behind the window, or no sinks
     int far0, piece_len;    // piece i covers queries far0 + i * piece_len ..
 };
-// Pieces of the far queries (those the first key tile's workgroup does not walk) for sinks > 0.
-struct SwaFar {
-    int pieces;
-    long far0, piece_len;
+// How the key/value gradients are cut.  far0: the first query the first key tile's workgroups leave
+// to the sinks' pieces.
+struct SwaCut {
+    int splits, part_rows, pieces, far0, piece_len;
 };
-inline SwaFar swa_far(long T, long window, int sinks) {
+// Workgroups of 128 keys fill the card once there are as many as compute units (256); with fewer, the
+// queries of a tile are cut into up to eight parts of at least two tiles of 64.  Pieces of the far
+// queries: up to two workgroups per compute unit, at least 128 queries and at most 64 pieces each.
+inline SwaCut swa_cut(long B, long T, long H, long Hkv, long window, int sinks) {
+    SwaCut c{1, 0, 0, 0, 0};
+    const long heads = B * Hkv, jobs = (T + kSwaKeyTile - 1) / kSwaKeyTile * heads;
+    const long seen = window + kSwaKeyTile < T ? window + kSwaKeyTile : T, tiles = (seen + 63) / 64 * (H / Hkv);
+    if (jobs < 256) {
+        const long want = 512 / jobs, s = want < tiles / 2 ? want : tiles / 2;
+        c.splits = (int)(s < 1 ? 1 : s < 8 ? s : 8);
+    }
     const long far0 = (kSwaKeyTile - 1 + window + 63) / 64 * 64;
-    if (sinks <= 0 || T <= far0) return {0, far0, 0};
-    long len = ((T - far0 + kSwaSinkPieces - 1) / kSwaSinkPieces + 63) / 64 * 64;
-    if (len < 512) len = 512;
-    return {(int)((T - far0 + len - 1) / len), far0, len};
+    c.far0 = (int)far0;
+    if (sinks > 0 && T > far0) {
+        const long want = heads < 512 ? 512 / heads : 1, most = (T - far0 + 127) / 128;
+        long n = want < most ? want : most;
+        n = n < 64 ? n : 64;
+        c.piece_len = (int)(((T - far0 + n - 1) / n + 63) / 64 * 64);
+        c.pieces = (int)((T - far0 + c.piece_len - 1) / c.piece_len);
+    }
+    c.part_rows = c.splits > 1 ? (int)T : c.pieces > 0 ? (int)(T < kSwaMaxSinks ? T : kSwaMaxSinks) : 0;
+    return c;
 }
 hipError_t swa_fwd_dispatch(int dtype_bf16, const SwaParams& p, hipStream_t s);
 hipError_t swa_bwd_dispatch(int dtype_bf16, const SwaParams& p, hipStream_t s);

@@ -9,9 +9,6 @@
 // operand as they stand: sixteen registers are rows 16 kk + {4h..4h+3, 8+4h..8+4h+3}, kk = 0, 1,
 // and its A operand is gathered from the LDS tile in that same order (ds_read_b64_tr_b16 for bf16,
 // one float per register for fp32).  No probability ever crosses lanes.
-//
-// An LDS tile is `rows` x CPR 16-byte pieces; piece c of row r sits at place c ^ swz(r), so that
-// neither sixteen rows read at one piece nor four rows read across 64 bytes share banks.
 #pragma once
 #include "gdr2_block_kernels.hpp"
 #include "gdr2_common.hpp"
@@ -20,6 +17,7 @@ namespace gdr2 {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 constexpr int kSwaThreads = 256, kSwaWaves = 4;
+constexpr long kSwaNarrowBelow = 256;  // workgroups of 128 queries: below one per compute unit, 64 queries each
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.0e38f;
 
@@ -34,32 +32,42 @@ struct Swa {
     static constexpr int ES = (int)sizeof(T), CPR = D * ES / 16;  // 16-byte pieces per row
     static constexpr int KK = CPR / 2;                            // contraction steps of a row
     static constexpr int DB = D / 32;                             // 32-column blocks of a row
-    static constexpr int BT = ES == 2 ? 64 : 32;                  // rows of a staged tile (16 KB at D = 128)
+    static constexpr int BT = D * ES > 256 ? 32 : 64;             // rows of a staged tile (at most 16 KB)
     static constexpr int NB = BT / 32;
     static constexpr int UNITS = BT * CPR / kSwaThreads;          // pieces a thread stages
     static_assert(UNITS * kSwaThreads == BT * CPR, "staging");
-    typedef i32x4 tile[BT * CPR];
 
-    static __device__ __forceinline__ int swz(int row) {
-        if constexpr (CPR == 8) return ((row >> 1) & 1) << 2 | ((row >> 2) & 3);
-        else return (row & 3) << 2 | ((row >> 2) & 3);
+    // 16-byte piece (row, c) of a tile.  kRows tiles are read by whole pieces of 16 rows at a time: padded
+    // by one piece, those rows fall in different banks.  kBoth tiles are also read by 64 bytes of four
+    // rows (add_rows): padded by four pieces, and piece c kept at c ^ (row / 4 % 4) inside its group of
+    // four, both reads are free of bank conflicts, at addresses that differ by constants.
+    static constexpr int kRows = 1, kBoth = 4;
+    template <int M> static constexpr int kPitch = CPR + M;
+    template <int M> using tile = i32x4[BT * (CPR + M)];
+    // piece 4 * group + c of a row
+    template <int M>
+    static __device__ __forceinline__ int at(int row, int group, int c) {
+        return row * kPitch<M> + 4 * group + (M == kBoth ? c ^ ((row >> 2) & 3) : c);
     }
-    static __device__ __forceinline__ int at(int row, int c) { return row * CPR + (c ^ swz(row)); }
 
-    // BT rows of a token tensor into registers: row r at base + r * stride bytes; rows at and
-    // behind `rows` are zero and not read
+    // BT rows of a token tensor into registers: row r at base + r * stride bytes.  Only the first `rows`
+    // (>= 1) exist; the last of them stands in for the others, which no live pair uses.
     static __device__ __forceinline__ void fetch(i32x4 (&u)[UNITS], const char* base, long stride, int rows) {
+        constexpr int RSTEP = kSwaThreads / CPR;  // rows between a thread's pieces
+        const unsigned st = (unsigned)stride, c = threadIdx.x % CPR * 16;  // strides stay below 2^24 + 1
+        const unsigned off = threadIdx.x / CPR * st + c, last = (rows - 1) * st + c;
 #pragma unroll
         for (int i = 0; i < UNITS; ++i) {
-            const int x = threadIdx.x + i * kSwaThreads, r = x / CPR, c = x % CPR;
-            u[i] = r < rows ? *(const i32x4*)(base + r * stride + c * 16) : i32x4{0, 0, 0, 0};
+            const unsigned o = off + i * RSTEP * st;
+            u[i] = *(const i32x4*)(base + (o < last ? o : last));
         }
     }
+    template <int M>
     static __device__ __forceinline__ void stage(i32x4* t, const i32x4 (&u)[UNITS]) {
-        constexpr int RSTEP = kSwaThreads / CPR;  // rows between a thread's pieces
-        const int r0 = threadIdx.x / CPR, c = threadIdx.x % CPR, p0 = at(r0, c);
+        constexpr int RSTEP = kSwaThreads / CPR;
+        const int r0 = threadIdx.x / CPR, c = threadIdx.x % CPR;
 #pragma unroll
-        for (int i = 0; i < UNITS; ++i) t[RSTEP % 16 ? at(r0 + i * RSTEP, c) : p0 + i * kSwaThreads] = u[i];
+        for (int i = 0; i < UNITS; ++i) t[at<M>(r0 + i * RSTEP, c / 4, c % 4)] = u[i];
     }
     // the B operand of 32 rows, kept in registers: piece 2 kk + h of the lane's row (null: zeros)
     static __device__ __forceinline__ void keep(i32x4 (&f)[KK], const char* row) {
@@ -78,15 +86,17 @@ struct Swa {
         }
     }
     // rows r0 .. r0 + 31 of a tile times the kept rows: C[r][n] = tile row . kept row
+    template <int M>
     static __device__ __forceinline__ f32x16 dots(const i32x4* t, int r0, const i32x4 (&f)[KK]) {
         const int l = lane_id(), row = r0 + (l & 31), h = l >> 5;
         f32x16 c = zero16();
 #pragma unroll
-        for (int kk = 0; kk < KK; ++kk) mma(c, t[at(row, 2 * kk + h)], f[kk]);
+        for (int kk = 0; kk < KK; ++kk) mma(c, t[at<M>(row, kk / 2, 2 * (kk % 2) + h)], f[kk]);
         return c;
     }
     // acc[db][d][n] += sum over the rows r0 + crow(r, h) of tile[row][32 db + d] w[r] (for bf16 the
     // weights are rounded to bf16: the products' inputs, relative error 2^-8 each, summed in fp32)
+    template <int M>
     static __device__ __forceinline__ void add_rows(f32x16 (&acc)[DB], const i32x4* t, int r0, const f32x16& w) {
         const int l = lane_id(), h = l >> 5;
         if constexpr (ES == 2) {
@@ -99,9 +109,9 @@ struct Swa {
                 const int ra = r0 + 16 * kk + 4 * h + (p >> 2), rb = ra + 8;
 #pragma unroll
                 for (int db = 0; db < DB; ++db) {
-                    const int c = 4 * db + 2 * sub + ((p & 3) >> 1);
-                    const bf16x4 lo = ds_read_tr4((const bf16*)(t + at(ra, c)) + 4 * (p & 1));
-                    const bf16x4 hi = ds_read_tr4((const bf16*)(t + at(rb, c)) + 4 * (p & 1));
+                    const int c = 2 * sub + ((p & 3) >> 1);
+                    const bf16x4 lo = ds_read_tr4((const bf16*)(t + at<M>(ra, db, c)) + 4 * (p & 1));
+                    const bf16x4 hi = ds_read_tr4((const bf16*)(t + at<M>(rb, db, c)) + 4 * (p & 1));
                     const bf16x8 a = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
                     acc[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc[db], 0, 0, 0);
                 }
@@ -113,14 +123,26 @@ struct Swa {
                 const int row = r0 + crow(r, h);
 #pragma unroll
                 for (int db = 0; db < DB; ++db) {
-                    const float a = ((const float*)(t + at(row, 8 * db + (n >> 2))))[n & 3];
+                    const float a = ((const float*)(t + at<M>(row, 2 * db + (n >> 4), (n >> 2) & 3)))[n & 3];
                     acc[db] = __builtin_amdgcn_mfma_f32_32x32x2f32(a, w[r], acc[db], 0, 0, 0);
                 }
             }
         }
     }
+    // The lane's values of its row (32 rows, lane column n = row), four channels at a time
+    template <typename F>
+    static __device__ __forceinline__ void each4(F&& f) {
+        const int h = lane_id() >> 5;
+#pragma unroll
+        for (int db = 0; db < DB; ++db)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f(db, 4 * j, 32 * db + 8 * j + 4 * h);  // block, first register, first channel
+    }
+    static __device__ __forceinline__ f32x4 four(const f32x16& a, int e) { return f32x4{a[e], a[e + 1], a[e + 2], a[e + 3]}; }
+
     // Writes 32 rows (lane column n = row) of D values, acc * mul, as whole rows through the wave's
-    // own 32 * CPR pieces of LDS: row n goes to out + n * stride bytes for n < rows.
+    // own kPut pieces of LDS: row n goes to out + n * stride bytes for n < rows.
+    static constexpr int kPut = 32 * kPitch<kRows>;
     static __device__ __forceinline__ void put_rows(const f32x16 (&acc)[DB], float mul, i32x4* buf, char* out,
                                                     long stride, int rows) {
         const int l = lane_id(), n = l & 31, h = l >> 5;
@@ -131,15 +153,15 @@ struct Swa {
                 const f32x4 x = {acc[db][4 * j] * mul, acc[db][4 * j + 1] * mul, acc[db][4 * j + 2] * mul, acc[db][4 * j + 3] * mul};
                 const int d0 = 32 * db + 8 * j + 4 * h, c = d0 * ES / 16;
                 if constexpr (ES == 2)
-                    *((bf16x4*)(buf + at(n, c)) + h) = bf16x4{(bf16)x[0], (bf16)x[1], (bf16)x[2], (bf16)x[3]};
+                    *((bf16x4*)(buf + at<kRows>(n, c / 4, c % 4)) + h) = bf16x4{(bf16)x[0], (bf16)x[1], (bf16)x[2], (bf16)x[3]};
                 else
-                    *(f32x4*)(buf + at(n, c)) = x;
+                    *(f32x4*)(buf + at<kRows>(n, c / 4, c % 4)) = x;
             }
         wave_sync();
 #pragma unroll
         for (int i = 0; i < 32 * CPR / 64; ++i) {
             const int x = l + i * 64, r = x / CPR, c = x % CPR;
-            const i32x4 u = buf[at(r, c)];
+            const i32x4 u = buf[at<kRows>(r, c / 4, c % 4)];
             if (r < rows) *(i32x4*)(out + r * stride + c * 16) = u;
         }
     }

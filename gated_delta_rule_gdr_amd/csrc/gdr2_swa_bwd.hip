@@ -11,25 +11,32 @@
 //   gdr2_swa_dkv_kernel   128 keys of one key/value head per workgroup, walking the query tiles of
 //                         its heads (four products per tile).
 // The sinks are seen by every later query: a key tile that walked them all would run many times
-// longer than the others, so the queries behind its window are cut into at most kSwaSinkPieces
-// pieces, each a workgroup of gdr2_swa_sink_kernel that leaves fp32 sums for the (at most 64)
-// sinks; the first key tile's workgroup adds them in order.
+// longer than the others, so the queries behind its window are cut into pieces, each a workgroup of
+// the second kernel that leaves fp32 sums for the (at most 64) sinks.  Where the key tiles alone do
+// not fill the card, the queries of a tile are cut into parts too.  gdr2_swa_reduce_kernel adds such
+// sums in a fixed order.
 #include "gdr2_swa.hpp"
 
 namespace gdr2 {
 
-template <typename T, int D>
+constexpr int kExactTiles = 4;  // key tiles (of 64) up to which delta is summed from the probabilities
+
+// KS = 2: 64 queries per workgroup, its halves walk alternate 32-key blocks (as in the forward).
+template <typename T, int D, int KS>
 __global__ __launch_bounds__(kSwaThreads, sizeof(T) * D > 256 ? 1 : 2) void gdr2_swa_dq_kernel(SwaParams p) {
     using S = Swa<T, D>;
-    constexpr int BT = S::BT, NB = S::NB;
-    constexpr int BQ = 32 * kSwaWaves;
-    __shared__ typename S::tile lds[4];
+    constexpr int BT = S::BT, NB = S::NB, QW = kSwaWaves / KS, BQ = 32 * QW;
+    constexpr int KM = S::kBoth, VM = S::kRows;
+    constexpr int KP = BT * S::template kPitch<KM>, VP = BT * S::template kPitch<VM>;
+    __shared__ i32x4 lds[2 * KP + 2 * VP];  // two key tiles, two value tiles
+    static_assert(sizeof(lds) >= (size_t)QW * S::kPut * 16, "output rows fit the tiles");
+    __shared__ float dsum[KS == 2 ? kSwaWaves : 1][32];
     const int l = lane_id(), wv = uniform_wave(), n = l & 31, h = l >> 5;
     const int nqt = (int)((p.T + BQ - 1) / BQ);
     const int work = xcd_swizzle(blockIdx.x, gridDim.x);
     const int qt = work % nqt, bh = work / nqt, b = bh / p.H, hd = bh % p.H, kvh = hd / (p.H / p.Hkv);
     const int L = swa_length(p, b);
-    const int Q0 = qt * BQ, q0 = Q0 + 32 * wv, i = q0 + n;
+    const int Q0 = qt * BQ, q0 = Q0 + 32 * (wv % QW), i = q0 + n, ks = wv / QW;
     const long qstr = (long)p.H * D * S::ES, kstr = (long)p.Hkv * D * S::ES;
     const char* kb = (const char*)p.k + ((long)b * p.T * p.Hkv + kvh) * D * S::ES;
     const char* vb = (const char*)p.v + ((long)b * p.T * p.Hkv + kvh) * D * S::ES;
@@ -66,45 +73,103 @@ __global__ __launch_bounds__(kSwaThreads, sizeof(T) * D > 256 ? 1 : 2) void gdr2
         const SwaTiles tl(p, BT, Q0, Q0 + BQ <= L ? Q0 + BQ - 1 : L - 1);
         i32x4 ku[S::UNITS], vu[S::UNITS];
         auto fetch = [&](int t) {
-            const int j0 = tl.start(t, BT);
-            const int rows = L - j0 < BT ? L - j0 : BT;
+            const int j0 = tl.start(t, BT), rows = L - j0 < BT ? L - j0 : BT;
             S::fetch(ku, kb + j0 * kstr, kstr, rows);
             S::fetch(vu, vb + j0 * kstr, kstr, rows);
         };
         fetch(0);
-        S::stage(lds[0], ku);
-        S::stage(lds[2], vu);
+        S::template stage<KM>(lds, ku);
+        S::template stage<VM>(lds + 2 * KP, vu);
         lds_barrier();
+        // the probabilities of the half's 32-key block k_ of the tile at j0, and dO . v
+        auto probs = [&](f32x16& s, f32x16& dp, int buf, int k_, int j0) {
+            s = S::template dots<KM>(lds + buf * KP, 32 * k_, qf);
+            dp = S::template dots<VM>(lds + 2 * KP + buf * VP, 32 * k_, gf);
+            if (j0 + BT - 1 > q0 || q0 + 31 - j0 >= p.window) {
+                edge_tile();
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (!swa_sees(p, i, j0 + 32 * k_ + crow(r, h))) s[r] = -INFINITY;
+            }
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[r] = exp2_f(s[r] * c - lse2);
+        };
+        // the wave has pairs in the tile at j0
+        auto meets = [&](int j0) { return j0 <= q0 + 31 && (q0 - (j0 + BT - 1) < p.window || j0 < p.sinks); };
+        // delta = sum_j p_ij dO_i . v_j also; formed from a 16-bit o it carries that rounding into every
+        // ds of the row, which shows where few keys share a row.  Queries with at most kExactTiles
+        // key tiles therefore walk them once more, for delta alone.
+        if (S::ES == 2 && tl.n <= kExactTiles) {
+            float sum = 0.f;
+#pragma unroll 1
+            for (int t = 0; t < tl.n; ++t) {
+                const int j0 = tl.start(t, BT);
+                if (meets(j0)) {
+#pragma unroll 1
+                    for (int u = 0; u < NB / KS; ++u) {
+                        f32x16 s, dp;
+                        probs(s, dp, 0, ks * (NB / KS) + u, j0);
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) sum += s[r] * dp[r];
+                    }
+                }
+                const int next = t + 1 < tl.n ? t + 1 : 0;
+                if (next != t) {
+                    fetch(next);
+                    lds_barrier();
+                    S::template stage<KM>(lds, ku);
+                    S::template stage<VM>(lds + 2 * KP, vu);
+                    lds_barrier();
+                }
+            }
+            sum += __shfl_xor(sum, 32);
+            delta = sum;
+            if constexpr (KS == 2) {
+                if (h == 0) dsum[wv][n] = sum;
+                __syncthreads();
+                delta = dsum[wv % QW][n] + dsum[wv % QW + QW][n];
+            }
+        }
         for_tiles(tl.n, [&](int t, auto buf_) {
             constexpr int cur = decltype(buf_)::value;
             if (t + 1 < tl.n) fetch(t + 1);
             const int j0 = tl.start(t, BT);
-            if (j0 <= q0 + 31 && (q0 - (j0 + BT - 1) < p.window || j0 < p.sinks)) {
-                const bool edge = j0 + BT - 1 > q0 || q0 + 31 - j0 >= p.window;
+            if (meets(j0)) {
 #pragma unroll
-                for (int k_ = 0; k_ < NB; ++k_) {
-                    f32x16 s = S::dots(lds[cur], 32 * k_, qf);
-                    const f32x16 dp = S::dots(lds[2 + cur], 32 * k_, gf);
-                    if (edge) {
-                        edge_tile();
+                for (int u = 0; u < NB / KS; ++u) {
+                    const int k_ = ks * (NB / KS) + u;
+                    f32x16 s, dp;
+                    probs(s, dp, cur, k_, j0);
 #pragma unroll
-                        for (int r = 0; r < 16; ++r)
-                            if (!swa_sees(p, i, j0 + 32 * k_ + crow(r, h))) s[r] = -INFINITY;
-                    }
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) s[r] = exp2_f(s[r] * c - lse2) * (dp[r] - delta);
-                    S::add_rows(acc, lds[cur], 32 * k_, s);
+                    for (int r = 0; r < 16; ++r) s[r] *= dp[r] - delta;
+                    S::template add_rows<KM>(acc, lds + cur * KP, 32 * k_, s);
                 }
             }
             if (t + 1 < tl.n) {
-                S::stage(lds[cur ^ 1], ku);
-                S::stage(lds[2 + (cur ^ 1)], vu);
+                S::template stage<KM>(lds + (cur ^ 1) * KP, ku);
+                S::template stage<VM>(lds + 2 * KP + (cur ^ 1) * VP, vu);
             }
             lds_barrier();
         });
     }
+    if constexpr (KS == 2) {
+        // the second half's sums, through LDS (the tiles are no longer read)
+        constexpr int PITCH = D + 4;
+        static_assert(sizeof(lds) >= sizeof(float) * (size_t)QW * 32 * PITCH, "sums of one half fit the tiles");
+        float* row = (float*)lds + ((wv % QW) * 32 + n) * PITCH;
+        if (ks == 1) S::each4([&](int db, int e, int d0) { *(f32x4*)(row + d0) = S::four(acc[db], e); });
+        __syncthreads();
+        if (ks == 0)
+            S::each4([&](int db, int e, int d0) {
+                const f32x4 x = *(const f32x4*)(row + d0);
+#pragma unroll
+                for (int c4 = 0; c4 < 4; ++c4) acc[db][e + c4] += x[c4];
+            });
+        __syncthreads();
+        if (ks == 1) return;
+    }
     const int rows = p.T - q0 >= 32 ? 32 : p.T > q0 ? p.T - q0 : 0;
-    S::put_rows(acc, p.scale, &lds[0][0] + wv * 32 * S::CPR,
+    S::put_rows(acc, p.scale, lds + wv * S::kPut,
                 (char*)p.dq + (((long)b * p.T + q0) * p.H + hd) * D * S::ES, qstr, rows);
     if (h == 0 && n < rows) p.delta[(long)bh * p.T + i] = delta;
 }
@@ -125,8 +190,8 @@ struct SwaKeys {
     __device__ __forceinline__ void step(const SwaParams& p, const i32x4* qt, const i32x4* gt, const float* ls, const float* dl,
                                          int r0, int i0, int j, bool edge, float c) {
         const int h = lane_id() >> 5;
-        f32x16 s = S::dots(qt, r0, kf);
-        f32x16 dp = S::dots(gt, r0, vf);
+        f32x16 s = S::template dots<S::kBoth>(qt, r0, kf);
+        f32x16 dp = S::template dots<S::kBoth>(gt, r0, vf);
         if (edge) {  // some pairs of the block are hidden
             edge_tile();
 #pragma unroll
@@ -142,8 +207,8 @@ struct SwaKeys {
                 dp[4 * r4 + e] = s[4 * r4 + e] * (dp[4 * r4 + e] - y[e]);
             }
         }
-        S::add_rows(dv, gt, r0, s);
-        S::add_rows(dk, qt, r0, dp);
+        S::template add_rows<S::kBoth>(dv, gt, r0, s);
+        S::template add_rows<S::kBoth>(dk, qt, r0, dp);
     }
 };
 
@@ -166,165 +231,170 @@ struct SwaQueries {
         else if (x < 2 * S::BT && r < rows) su = p.delta[at];
     }
     __device__ __forceinline__ void stage(i32x4* qt, i32x4* gt, float* sc) const {
-        S::stage(qt, qu);
-        S::stage(gt, gu);
+        S::template stage<S::kBoth>(qt, qu);
+        S::template stage<S::kBoth>(gt, gu);
         if (threadIdx.x < 2 * S::BT) sc[threadIdx.x] = su;
     }
 };
 
+// Two kinds of workgroups.  Main ones: 128 keys, 32 per wave, against part `split` of the tiles of the
+// queries that see them, head by head.  The first sink_wgs ones: the sinks (at most 64 keys) against one
+// piece of the far queries; a wave takes key block wv / NB and query block wv % NB of every tile.
 template <typename T, int D>
 __global__ __launch_bounds__(kSwaThreads, sizeof(T) * D > 128 ? 1 : 2) void gdr2_swa_dkv_kernel(SwaParams p) {
     using S = Swa<T, D>;
     constexpr int BT = S::BT, NB = S::NB;
     static_assert(kSwaKeyTile == 32 * kSwaWaves, "a wave holds 32 keys");
-    __shared__ typename S::tile lds[4];  // queries and cotangents, two of each
+    __shared__ typename S::template tile<S::kBoth> lds[4];  // queries and cotangents, two of each
     __shared__ float sc[2][2 * BT];
-    const int l = lane_id(), wv = uniform_wave(), n = l & 31, h = l >> 5;
-    const int nkt = (int)((p.T + kSwaKeyTile - 1) / kSwaKeyTile);
-    const int work = xcd_swizzle(blockIdx.x, gridDim.x);
-    const int kt = work % nkt, bh = work / nkt, b = bh / p.Hkv, kvh = bh % p.Hkv, G = p.H / p.Hkv;
-    const int L = swa_length(p, b);
-    const int K0 = kt * kSwaKeyTile, k0 = K0 + 32 * wv, j = k0 + n;
+    static_assert(sizeof(lds) >= (size_t)kSwaWaves * S::kPut * 16, "output rows fit the tiles");
+    static_assert(sizeof(lds) >= 2 * 32 * D * 2 * sizeof(float), "partial sums of two waves fit the tiles");
+    const int l = lane_id(), wv = uniform_wave(), n = l & 31, G = p.H / p.Hkv;
+    const int sink_wgs = p.pieces * p.B * p.Hkv;
+    const bool far = (int)blockIdx.x < sink_wgs;
+    int bh, K0, split = 0, piece = 0;
+    if (far) {
+        piece = blockIdx.x % p.pieces;
+        bh = blockIdx.x / p.pieces;
+        K0 = 0;
+    } else {
+        const int nkt = (p.T + kSwaKeyTile - 1) / kSwaKeyTile;
+        const int work = xcd_swizzle(blockIdx.x - sink_wgs, gridDim.x - sink_wgs), job = work / p.splits;
+        split = work % p.splits;
+        K0 = job % nkt * kSwaKeyTile;
+        bh = job / nkt;
+    }
+    const int b = bh / p.Hkv, kvh = bh % p.Hkv, L = swa_length(p, b);
+    const int k0 = K0 + 32 * (far ? wv / NB : wv), j = k0 + n;
+    const bool mine = !far || k0 < p.sinks;  // a key block without a sink has no far queries
     const long kstr = (long)p.Hkv * D * S::ES;
-    const long koff = (((long)b * p.T + j) * p.Hkv + kvh) * D * S::ES;
     const float c = p.scale * kLog2e;
+    const int ia = p.far0 + piece * p.piece_len;
+    if (far && ia >= L) return;  // the reduction skips this piece too
+    // queries from .. to, in `per` tiles per head; the queries that see the tile's last key, and, with
+    // sinks, for the first tile those up to the far ones
+    const int from = far ? ia : K0, seen = far ? ia + p.piece_len : K0 == 0 && p.sinks > 0 ? p.far0 : K0 + kSwaKeyTile - 1 + p.window;
+    const int to = seen < L ? seen : L;
+    const bool key = j < L && (!far || j < p.sinks);
+    const long koff = (((long)b * p.T + j) * p.Hkv + kvh) * D * S::ES;
     SwaKeys<T, D> ks;
-    ks.init(j < L ? (const char*)p.k + koff : nullptr, j < L ? (const char*)p.v + koff : nullptr);
+    ks.init(key ? (const char*)p.k + koff : nullptr, key ? (const char*)p.v + koff : nullptr);
     if (K0 < L) {
-        // the queries that see the tile's last key; with sinks, the first tile's go on to the far ones
-        const int seen = kt == 0 && p.sinks > 0 ? p.far0 : K0 + kSwaKeyTile - 1 + p.window;
-        const int i_end = seen < L ? seen : L;
-        const int t0 = K0 / BT, per = (i_end + BT - 1) / BT - t0, nt = per * G;
+        const int per = (to - from + BT - 1) / BT, all = per * G;
+        const int parts = far ? 1 : p.splits;
+        const int t0 = (int)((long)all * split / parts), nt = (int)((long)all * (split + 1) / parts) - t0;
         SwaQueries<T, D> qs;
-        auto fetch = [&](int t) { qs.fetch(p, b, kvh * G + t / per, (t0 + t % per) * BT, L); };
-        fetch(0);
-        qs.stage(lds[0], lds[2], sc[0]);
+        auto fetch = [&](int t) { qs.fetch(p, b, kvh * G + (t0 + t) / per, from + (t0 + t) % per * BT, L); };
+        if (nt > 0) {
+            fetch(0);
+            qs.stage(lds[0], lds[2], sc[0]);
+        }
         lds_barrier();
         for_tiles(nt, [&](int t, auto buf_) {
             constexpr int cur = decltype(buf_)::value;
             if (t + 1 < nt) fetch(t + 1);
-            const int i0 = (t0 + t % per) * BT;
+            const int i0 = from + (t0 + t) % per * BT;
 #pragma unroll
             for (int r = 0; r < NB; ++r) {
-                const int ia = i0 + 32 * r;
-                if (ia + 31 >= k0 && (ia - (k0 + 31) < p.window || k0 < p.sinks))
+                const int ib = i0 + 32 * r;
+                if (mine && (!far || r == wv % NB) && ib + 31 >= k0 && (ib - (k0 + 31) < p.window || k0 < p.sinks))
                     ks.step(p, lds[cur], lds[2 + cur], sc[cur], sc[cur] + BT, 32 * r, i0, j,
-                            ia < k0 + 31 || ia + 31 - k0 >= p.window, c);
+                            ib < k0 + 31 || ib + 31 - k0 >= p.window, c);
             }
             if (t + 1 < nt) qs.stage(lds[cur ^ 1], lds[2 + (cur ^ 1)], sc[cur ^ 1]);
             lds_barrier();
         });
     }
-    // the sinks' sums over the far queries, piece by piece
-    if (kt == 0 && p.pieces > 0 && k0 < p.sinks) {
-        for (int q = 0; q < p.pieces; ++q) {
-            if (p.far0 + q * p.piece_len >= L) break;
-            const float* part = p.sink_part + (((long)q * p.B * p.Hkv + bh) * 2 * kSwaMaxSinks + j) * D;
-#pragma unroll
-            for (int db = 0; db < S::DB; ++db)
-#pragma unroll
-                for (int r4 = 0; r4 < 4; ++r4) {
-                    const f32x4 x = *(const f32x4*)(part + 32 * db + 8 * r4 + 4 * h);
-                    const f32x4 y = *(const f32x4*)(part + (long)kSwaMaxSinks * D + 32 * db + 8 * r4 + 4 * h);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        ks.dk[db][4 * r4 + e] += x[e];
-                        ks.dv[db][4 * r4 + e] += y[e];
-                    }
-                }
+    if (far) {
+        // two query blocks of one key block: the second wave's sums through LDS
+        float* buf = (float*)&lds[0][0] + (wv / NB) * 2 * 32 * D + n * D;
+        if constexpr (NB == 2) {
+            if (mine && wv % NB == 1)
+                S::each4([&](int db, int e, int d0) {
+                    *(f32x4*)(buf + d0) = S::four(ks.dk[db], e);
+                    *(f32x4*)(buf + 32 * D + d0) = S::four(ks.dv[db], e);
+                });
+            __syncthreads();
         }
+        if (!mine || wv % NB != 0) return;
+        float* part = p.sink_part + (((long)piece * p.B * p.Hkv + bh) * 2 * kSwaMaxSinks + j) * D;
+        S::each4([&](int db, int e, int d0) {
+            f32x4 x = S::four(ks.dk[db], e), y = S::four(ks.dv[db], e);
+            if constexpr (NB == 2) {
+                x += *(const f32x4*)(buf + d0);
+                y += *(const f32x4*)(buf + 32 * D + d0);
+            }
+            *(f32x4*)(part + d0) = x;
+            *(f32x4*)(part + (long)kSwaMaxSinks * D + d0) = y;
+        });
+        return;
     }
     const int rows = p.T - k0 >= 32 ? 32 : p.T > k0 ? p.T - k0 : 0;
+    if (p.splits > 1 || (p.pieces > 0 && k0 < kSwaMaxSinks)) {  // fp32 sums for the reduction
+        if (n < rows) {
+            const long set = (long)p.B * p.part_rows * p.Hkv * D;
+            float* part = p.key_part + (long)split * 2 * set + (((long)b * p.part_rows + j) * p.Hkv + kvh) * D;
+            S::each4([&](int db, int e, int d0) {
+                *(f32x4*)(part + d0) = S::four(ks.dk[db], e);
+                *(f32x4*)(part + set + d0) = S::four(ks.dv[db], e);
+            });
+        }
+        return;
+    }
     const long ooff = (((long)b * p.T + k0) * p.Hkv + kvh) * D * S::ES;
-    i32x4* buf = &lds[0][0] + wv * 32 * S::CPR;
+    i32x4* buf = &lds[0][0] + wv * S::kPut;
     S::put_rows(ks.dk, p.scale, buf, (char*)p.dk + ooff, kstr, rows);
     wave_sync();
     S::put_rows(ks.dv, 1.f, buf, (char*)p.dv + ooff, kstr, rows);
 }
 
-// Sums over one piece of the far queries for the sinks: wave w takes the queries of 32-row block
-// w % NB of every tile and the keys of block w / NB (kSwaMaxSinks: two blocks).
-template <typename T, int D>
-__global__ __launch_bounds__(kSwaThreads, sizeof(T) * D > 128 ? 1 : 2) void gdr2_swa_sink_kernel(SwaParams p) {
-    using S = Swa<T, D>;
-    constexpr int BT = S::BT, NB = S::NB;
-    __shared__ typename S::tile lds[4];
-    __shared__ float sc[2][2 * BT];
-    static_assert(sizeof(lds) >= 2 * 32 * D * 2 * sizeof(float), "partial sums of two waves fit the tiles");
-    const int l = lane_id(), wv = uniform_wave(), n = l & 31, h = l >> 5;
-    const int piece = blockIdx.x % p.pieces, bh = blockIdx.x / p.pieces, b = bh / p.Hkv, kvh = bh % p.Hkv, G = p.H / p.Hkv;
-    const int L = swa_length(p, b);
-    const int ia = p.far0 + piece * p.piece_len;
-    if (ia >= L) return;  // the first key tile skips this piece too
-    const int ib = ia + p.piece_len < L ? ia + p.piece_len : L;
-    const int rb = wv % NB, key0 = 32 * (wv / NB);
-    const int j = key0 + n;
-    const bool mine = key0 < p.sinks;
-    const float c = p.scale * kLog2e;
-    const long koff = (((long)b * p.T + j) * p.Hkv + kvh) * D * S::ES;
-    // far queries lie behind far0 > the sinks, so a sink's row exists; keys behind the sinks are zero
-    const bool key = j < p.sinks && j < L;
-    SwaKeys<T, D> ks;
-    ks.init(key ? (const char*)p.k + koff : nullptr, key ? (const char*)p.v + koff : nullptr);
-    const int per = (ib - ia + BT - 1) / BT, nt = per * G;
-    SwaQueries<T, D> qs;
-    auto fetch = [&](int t) { qs.fetch(p, b, kvh * G + t / per, ia + t % per * BT, L); };
-    fetch(0);
-    qs.stage(lds[0], lds[2], sc[0]);
-    lds_barrier();
-    for_tiles(nt, [&](int t, auto buf_) {
-        constexpr int cur = decltype(buf_)::value;
-        if (t + 1 < nt) fetch(t + 1);
-        if (mine) ks.step(p, lds[cur], lds[2 + cur], sc[cur], sc[cur] + BT, 32 * rb, ia + t % per * BT, j, true, c);
-        if (t + 1 < nt) qs.stage(lds[cur ^ 1], lds[2 + (cur ^ 1)], sc[cur ^ 1]);
-        lds_barrier();
-    });
-    // two query blocks of one key block: the second wave's sums through LDS
-    float* buf = (float*)&lds[0][0] + (wv / NB) * 2 * 32 * D;
-    auto place = [&](int db, int r4) { return n * D + 32 * db + 8 * r4 + 4 * h; };
-    if constexpr (NB == 2) {
-        if (mine && rb == 1) {
-#pragma unroll
-            for (int db = 0; db < S::DB; ++db)
-#pragma unroll
-                for (int r4 = 0; r4 < 4; ++r4) {
-                    const int e = 4 * r4;
-                    *(f32x4*)(buf + place(db, r4)) = f32x4{ks.dk[db][e], ks.dk[db][e + 1], ks.dk[db][e + 2], ks.dk[db][e + 3]};
-                    *(f32x4*)(buf + 32 * D + place(db, r4)) = f32x4{ks.dv[db][e], ks.dv[db][e + 1], ks.dv[db][e + 2], ks.dv[db][e + 3]};
-                }
-        }
-        __syncthreads();
+// dk and dv of the first part_rows rows: the parts of their queries in order, then, for the sinks, the
+// pieces of the far queries.  Four channels per thread.
+template <typename T>
+__global__ __launch_bounds__(256) void gdr2_swa_reduce_kernel(SwaParams p) {
+    const int d4 = p.d / 4;
+    const long n4 = (long)p.B * p.part_rows * p.Hkv * d4, x = (long)blockIdx.x * 256 + threadIdx.x;
+    if (x >= n4) return;
+    const int d0 = (int)(x % d4) * 4, kvh = (int)(x / d4 % p.Hkv), j = (int)(x / d4 / p.Hkv % p.part_rows);
+    const int b = (int)(x / d4 / p.Hkv / p.part_rows);
+    f32x4 dk = {0, 0, 0, 0}, dv = {0, 0, 0, 0};
+    for (int s = 0; s < p.splits; ++s) {
+        const f32x4* part = (const f32x4*)p.key_part + (long)s * 2 * n4 + x;
+        dk += part[0];
+        dv += part[n4];
     }
-    if (!mine || rb != 0) return;
-    float* part = p.sink_part + (((long)piece * p.B * p.Hkv + bh) * 2 * kSwaMaxSinks + key0) * D;
-#pragma unroll
-    for (int db = 0; db < S::DB; ++db)
-#pragma unroll
-        for (int r4 = 0; r4 < 4; ++r4) {
-            const int e = 4 * r4;
-            f32x4 x = {ks.dk[db][e], ks.dk[db][e + 1], ks.dk[db][e + 2], ks.dk[db][e + 3]};
-            f32x4 y = {ks.dv[db][e], ks.dv[db][e + 1], ks.dv[db][e + 2], ks.dv[db][e + 3]};
-            if constexpr (NB == 2) {
-                x += *(const f32x4*)(buf + place(db, r4));
-                y += *(const f32x4*)(buf + 32 * D + place(db, r4));
-            }
-            *(f32x4*)(part + place(db, r4)) = x;
-            *(f32x4*)(part + (long)kSwaMaxSinks * D + place(db, r4)) = y;
+    if (j < p.sinks) {
+        const int L = swa_length(p, b);
+        for (int q = 0; q < p.pieces && p.far0 + q * p.piece_len < L; ++q) {
+            const float* part = p.sink_part + ((((long)q * p.B + b) * p.Hkv + kvh) * 2 * kSwaMaxSinks + j) * p.d + d0;
+            dk += *(const f32x4*)part;
+            dv += *(const f32x4*)(part + (long)kSwaMaxSinks * p.d);
         }
+    }
+    const long o = (((long)b * p.T + j) * p.Hkv + kvh) * p.d + d0;
+    store4((T*)p.dk + o, dk * p.scale);
+    store4((T*)p.dv + o, dv);
 }
 
 template <typename T, int D>
 static hipError_t launch_swa_bwd(const SwaParams& p, hipStream_t s) {
-    const long gq = (long)((p.T + 127) / 128) * p.B * p.H, gk = (long)((p.T + kSwaKeyTile - 1) / kSwaKeyTile) * p.B * p.Hkv;
-    hipLaunchKernelGGL((gdr2_swa_dq_kernel<T, D>), dim3((unsigned)gq), dim3(kSwaThreads), 0, s, p);
+    const long heads = (long)p.B * p.H, wide = (p.T + 127) / 128 * heads, narrow = (p.T + 63) / 64 * heads;
+    bool done = false;
+    if constexpr (Swa<T, D>::NB == 2) {
+        if (wide < kSwaNarrowBelow) {
+            hipLaunchKernelGGL((gdr2_swa_dq_kernel<T, D, 2>), dim3((unsigned)narrow), dim3(kSwaThreads), 0, s, p);
+            done = true;
+        }
+    }
+    if (!done) hipLaunchKernelGGL((gdr2_swa_dq_kernel<T, D, 1>), dim3((unsigned)wide), dim3(kSwaThreads), 0, s, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (p.pieces > 0) {
-        hipLaunchKernelGGL((gdr2_swa_sink_kernel<T, D>), dim3((unsigned)((long)p.pieces * p.B * p.Hkv)), dim3(kSwaThreads), 0, s, p);
-        e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    hipLaunchKernelGGL((gdr2_swa_dkv_kernel<T, D>), dim3((unsigned)gk), dim3(kSwaThreads), 0, s, p);
+    const long bk = (long)p.B * p.Hkv, main = (p.T + kSwaKeyTile - 1) / kSwaKeyTile * bk * p.splits;
+    hipLaunchKernelGGL((gdr2_swa_dkv_kernel<T, D>), dim3((unsigned)(main + p.pieces * bk)), dim3(kSwaThreads), 0, s, p);
+    e = hipGetLastError();
+    if (e != hipSuccess || p.part_rows == 0) return e;
+    const long n4 = bk * p.part_rows * (D / 4);
+    hipLaunchKernelGGL((gdr2_swa_reduce_kernel<T>), dim3((unsigned)((n4 + 255) / 256)), dim3(256), 0, s, p);
     return hipGetLastError();
 }
 
