@@ -180,17 +180,26 @@ def load_library():
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+# the current stream's handle without building a torch.cuda.Stream object, where torch offers it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(dev):
-    return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+    if _raw_stream is not None:
+        return _raw_stream(dev.index)
+    return torch.cuda.current_stream(dev).cuda_stream
 
 
 def _run(fn_name, dev, fn, *args):
     """Call a C entry point with dev current and its current stream appended; raise on error."""
-    with torch.cuda.device(dev):
+    if torch.cuda.current_device() == dev.index:
         st = fn(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream(dev))
     _check(fn_name, st)
 
 
@@ -241,6 +250,8 @@ def _need(name, t, shape, dtype, dev, optional=False):
         raise ValueError(f"{name} is required")
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
+    if t.shape == shape and t.dtype == dtype and t.is_contiguous() and t.device == dev:
+        return
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {tuple(shape)}")
     if t.dtype != dtype:

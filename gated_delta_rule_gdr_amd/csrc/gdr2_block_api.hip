@@ -38,7 +38,7 @@ gdr2_status check_norm(int64_t rows, int64_t D) {
 gdr2_status check_glr(int64_t B, int64_t T, int64_t D) {
     if (B < 0 || T < 0 || D < 0 || T > ((int64_t)1 << 37) || D > ((int64_t)1 << 30)) return GDR2_E_SHAPE;
     if (D < 8 || D % 8) return GDR2_E_UNSUPPORTED;
-    const int64_t nseg = gdr2::glr_segments(T), strips = gdr2::glr_strips(D);
+    const int64_t nseg = gdr2::glr_segments(T, gdr2::kGlrBwdSeg), strips = gdr2::glr_strips(D);
     if (!prod_le(B, strips, kMaxGrid) || !prod_le(B * strips, nseg, kMaxGrid)) return GDR2_E_SHAPE;
     return GDR2_OK;
 }
@@ -46,11 +46,12 @@ struct GlrWs {
     size_t states, pub, ticket, total;  // offsets; the forward's layout (the backward has no states)
 };
 GlrWs glr_layout(int64_t B, int64_t T, int64_t D, bool with_states) {
-    const size_t nseg = gdr2::glr_segments(T), ch = gdr2::glr_strips(D) * gdr2::kGlrCh;
+    const size_t nbwd = gdr2::glr_segments(T, gdr2::kGlrBwdSeg), ch = gdr2::glr_strips(D) * gdr2::kGlrCh;
+    const size_t nseg = with_states ? gdr2::glr_segments(T, gdr2::kGlrFwdSeg) : nbwd;
     GlrWs w{};
     size_t off = 0;
     auto take = [&](size_t n) { const size_t o = off; off += round_up(n, 256); return o; };
-    w.states = take(with_states ? (size_t)B * nseg * D * 4 : 0);
+    w.states = take(with_states ? (size_t)B * nbwd * D * 4 : 0);
     w.pub = take(nseg > 1 ? (size_t)B * (nseg + nseg / gdr2::kGlrGroup) * ch * 8 : 0);
     w.ticket = take(nseg > 1 ? 4 : 0);
     w.total = off;
@@ -170,10 +171,10 @@ size_t gdr2_glr_bwd_workspace_bytes(int64_t B, int64_t T, int64_t D) {
 }
 
 static gdr2::GlrParams glr_params(int64_t B, int64_t T, int64_t D, const void* x, const float* la,
-                                  const GlrWs& w, void* ws) {
+                                  int seg, const GlrWs& w, void* ws) {
     gdr2::GlrParams p{};
     p.B = (int)B; p.T = T; p.D = D; p.x = x; p.la = la;
-    p.nseg = (int)gdr2::glr_segments(T);
+    p.nseg = (int)gdr2::glr_segments(T, seg);
     p.nstrip = (int)gdr2::glr_strips(D);
     p.pub = (unsigned long long*)((char*)ws + w.pub);
     p.ticket = (unsigned*)((char*)ws + w.ticket);
@@ -195,7 +196,7 @@ gdr2_status gdr2_glr_fwd(int64_t B, int64_t T, int64_t D, gdr2_dtype dt, const v
     const Range ins[] = {{x, n * esize(dt)}, {log_a, n * 4}, {h0, s}};
     const Range outs[] = {{h, n * esize(dt)}, {h_T, s}, {workspace, w.total}};
     if (any_alias(outs, 3, ins, 3)) return GDR2_E_ALIAS;
-    gdr2::GlrParams p = glr_params(B, T, D, x, log_a, w, workspace);
+    gdr2::GlrParams p = glr_params(B, T, D, x, log_a, gdr2::kGlrFwdSeg, w, workspace);
     p.h0 = h0; p.h = h; p.hT = h_T; p.states = (float*)((char*)workspace + w.states);
     return status_of(gdr2::glr_dispatch(dt == GDR2_BF16, false, p, (hipStream_t)stream));
 }
@@ -217,7 +218,7 @@ gdr2_status gdr2_glr_bwd(int64_t B, int64_t T, int64_t D, gdr2_dtype dt, const v
     const Range ins[] = {{x, n * esize(dt)}, {log_a, n * 4}, {fwd_workspace, f.total}, {dh, n * esize(dt)}, {dh_T, s}};
     const Range outs[] = {{dx, n * esize(dt)}, {dlog_a, n * 4}, {dh0, s}, {workspace, w.total}};
     if (any_alias(outs, 4, ins, 5)) return GDR2_E_ALIAS;
-    gdr2::GlrParams p = glr_params(B, T, D, x, log_a, w, workspace);
+    gdr2::GlrParams p = glr_params(B, T, D, x, log_a, gdr2::kGlrBwdSeg, w, workspace);
     p.states = (float*)((char*)fwd_workspace + f.states);
     p.dh = dh; p.dhT = dh_T; p.dx = dx; p.dla = dlog_a; p.dh0 = dh0;
     return status_of(gdr2::glr_dispatch(dt == GDR2_BF16, true, p, (hipStream_t)stream));

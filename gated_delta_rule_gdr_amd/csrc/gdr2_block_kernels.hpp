@@ -25,7 +25,7 @@ long norm_bwd_blocks(long rows, int D);
 hipError_t norm_dispatch(int dtype_bf16, bool bwd, const NormParams& p, hipStream_t s);
 
 // Gated linear recurrence h_t = exp(log_a_t) h_{t-1} + x_t per channel.
-constexpr int kGlrSeg = 128;    // tokens of a segment: one workgroup's share of the time axis
+constexpr int kGlrFwdSeg = 256, kGlrBwdSeg = 128;  // tokens of a segment: a workgroup's share of the time axis
 constexpr int kGlrCh = 64;      // channels of a workgroup
 constexpr int kGlrGroup = 16;   // segments between two published running states
 struct GlrParams {
@@ -36,7 +36,7 @@ struct GlrParams {
     const float* h0;      // [B][D] or null
     void* h;              // [B][T][D] input dtype
     float* hT;            // [B][D] or null
-    float* states;        // [B][nseg][D]: the state entering each segment
+    float* states;        // [B][segments of the backward][D]: the state entering each
     const void* dh;       // backward: cotangent of h
     const float* dhT;     // [B][D] or null
     void* dx;             // [B][T][D] input dtype
@@ -46,7 +46,7 @@ struct GlrParams {
                               // [B][nseg / kGlrGroup][..] published running states
     unsigned* ticket;
 };
-inline long glr_segments(long T) { return T <= 0 ? 1 : (T + kGlrSeg - 1) / kGlrSeg; }
+inline __host__ __device__ long glr_segments(long T, int seg) { return T <= 0 ? 1 : (T + seg - 1) / seg; }
 inline long glr_strips(long D) { return (D + kGlrCh - 1) / kGlrCh; }
 hipError_t glr_dispatch(int dtype_bf16, bool bwd, const GlrParams& p, hipStream_t s);
 struct GlrStepParams {

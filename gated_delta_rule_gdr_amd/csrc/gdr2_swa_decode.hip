@@ -24,7 +24,7 @@ constexpr int kDecStep = kDecTile * kDecWaves;      // slots of a workgroup's st
 constexpr float kDecLowest = -3.0e38f, kDecLog2e = 1.4426950408889634f;
 
 template <typename T, int D>
-__global__ __launch_bounds__(kDecThreads) void gdr2_swa_decode_kernel(SwaDecodeParams p) {
+__global__ __launch_bounds__(kDecThreads, 2) void gdr2_swa_decode_kernel(SwaDecodeParams p) {
     constexpr int ES = (int)sizeof(T), DPL = D / 16, KS = D * ES / 64;  // KS: 64-byte steps of a row
     constexpr int PITCH = D + 4;
     __shared__ float osum[kDecWaves][kDecHeads][PITCH];
@@ -170,27 +170,45 @@ __global__ __launch_bounds__(kDecThreads) void gdr2_swa_decode_kernel(SwaDecodeP
     }
 }
 
-// Joins the parts of one (sequence, key/value head, head group) in order.
+// Joins the parts of one head: thread groups of D / 4 lanes take every kGroups-th part, four channels per
+// lane, then the groups in order.
 template <typename T, int D>
 __global__ __launch_bounds__(kDecThreads) void gdr2_swa_decode_join_kernel(SwaDecodeParams p) {
+    constexpr int LANES = D / 4, kGroups = kDecThreads / LANES;
+    __shared__ f32x4 osum[kGroups][LANES];
+    __shared__ float stat[kGroups][2];
     const int G = p.H / p.Hkv, groups = (G + kDecHeads - 1) / kDecHeads;
-    const int job = blockIdx.x, grp = job % groups, kvh = job / groups % p.Hkv, sq = job / groups / p.Hkv;
-    const int h0 = kvh * G + grp * kDecHeads, heads = G - grp * kDecHeads < kDecHeads ? G - grp * kDecHeads : kDecHeads;
+    const int sq = blockIdx.x / p.H, head = blockIdx.x % p.H, kvh = head / G, in = head % G;
+    const long job = ((long)sq * p.Hkv + kvh) * groups + in / kDecHeads, stride = (long)kDecHeads * (D + 4);
+    const float* part = p.part + job * p.splits * stride + (in % kDecHeads) * (D + 4);
+    const int grp = threadIdx.x / LANES, ln = threadIdx.x % LANES;
     const bool any = p.pos[sq] >= 0;
-    for (int x = threadIdx.x; x < heads * (D / 4); x += kDecThreads) {
-        const int hd = x / (D / 4), d = 4 * (x % (D / 4));
-        const float* part = p.part + ((long)job * p.splits * kDecHeads + hd) * (D + 4);
-        float M = kDecLowest, Z = 0.f;
-        for (int s = 0; s < p.splits; ++s) M = fmaxf(M, part[(long)s * kDecHeads * (D + 4) + D]);
-        f32x4 o = {0, 0, 0, 0};
-        for (int s = 0; s < p.splits; ++s) {
-            const float* q = part + (long)s * kDecHeads * (D + 4);
-            const float f = __builtin_amdgcn_exp2f(q[D] - M);
-            Z += q[D + 1] * f;
-            o += *(const f32x4*)(q + d) * f;
-        }
-        store4((T*)p.o + ((long)sq * p.H + h0 + hd) * D + d, any ? o * (1.f / Z) : f32x4{0, 0, 0, 0});
+    float M = kDecLowest, Z = 0.f;
+    f32x4 o = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int s = grp; s < p.splits; s += kGroups) {
+        const float* q = part + s * stride;
+        const f32x4 x = *(const f32x4*)(q + 4 * ln);
+        const float m = q[D], z = q[D + 1], mn = fmaxf(M, m);
+        const float f0 = __builtin_amdgcn_exp2f(M - mn), f1 = __builtin_amdgcn_exp2f(m - mn);
+        M = mn;
+        Z = Z * f0 + z * f1;
+        o = o * f0 + x * f1;
     }
+    osum[grp][ln] = o;
+    if (ln == 0) {
+        stat[grp][0] = M;
+        stat[grp][1] = Z;
+    }
+    __syncthreads();
+    if (grp != 0) return;
+    for (int g = 1; g < kGroups; ++g) {
+        const float m = stat[g][0], mn = fmaxf(M, m), f0 = __builtin_amdgcn_exp2f(M - mn), f1 = __builtin_amdgcn_exp2f(m - mn);
+        M = mn;
+        Z = Z * f0 + stat[g][1] * f1;
+        o = o * f0 + osum[g][ln] * f1;
+    }
+    store4((T*)p.o + ((long)sq * p.H + head) * D + 4 * ln, any ? o * (1.f / Z) : f32x4{0, 0, 0, 0});
 }
 
 // Parts per (sequence, key/value head, head group): enough workgroups for two per compute unit,
@@ -209,7 +227,7 @@ static hipError_t launch_decode(const SwaDecodeParams& p, hipStream_t s) {
     hipLaunchKernelGGL((gdr2_swa_decode_kernel<T, D>), dim3((unsigned)(jobs * p.splits)), dim3(kDecThreads), 0, s, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
-    hipLaunchKernelGGL((gdr2_swa_decode_join_kernel<T, D>), dim3((unsigned)jobs), dim3(kDecThreads), 0, s, p);
+    hipLaunchKernelGGL((gdr2_swa_decode_join_kernel<T, D>), dim3((unsigned)((long)p.N * p.H)), dim3(kDecThreads), 0, s, p);
     return hipGetLastError();
 }
 
