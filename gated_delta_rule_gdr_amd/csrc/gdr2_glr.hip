@@ -70,11 +70,17 @@ __device__ __forceinline__ float word_lo(unsigned long long w) { return __builti
 __device__ __forceinline__ void publish(unsigned long long* p, unsigned long long w) {
     __hip_atomic_store(p, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
+// Waits of a call that has its workspace to itself end within microseconds.  The bound (some tenths of a
+// second) is for a workspace that another call clears meanwhile: such calls return NaN, not never.
+constexpr int kAwaitPolls = 1 << 18;
 __device__ __forceinline__ unsigned long long await(unsigned long long* p) {
-    unsigned long long w;
-    while ((w = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) == kUnpublished)
+    unsigned long long w = kUnpublished;
+    for (int i = 0; i < kAwaitPolls; ++i) {
+        w = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (w != kUnpublished) break;
         __builtin_amdgcn_s_sleep(2);
-    return w;
+    }
+    return w;  // (kUnpublished reads as a pair of NaN)
 }
 
 template <int W>
@@ -86,7 +92,8 @@ struct GlrSmem {
 };
 
 // Where the workgroup stands in the scan: its place `ord` (0 = first segment of the scan), strip
-// and batch row.  Tickets count the strips of one place before the next place.
+// and batch row.  Tickets count the strips of one place before the next place.  One behind the last
+// (again: a workspace that another call uses) is nobody's: ord < 0.
 struct GlrPlace {
     int ord, strip, b;
 };
@@ -99,6 +106,7 @@ __device__ __forceinline__ GlrPlace glr_place(const GlrParams& p, GlrSmem<W>& sm
         __syncthreads();
         t = sm.ticket;
     }
+    if (t >= gridDim.x) return {-1, 0, 0};
     const unsigned per = (unsigned)p.nstrip * (unsigned)p.B, r = t % per;
     return {(int)(t / per), (int)(r % (unsigned)p.nstrip), (int)(r / (unsigned)p.nstrip)};
 }
@@ -204,6 +212,7 @@ __global__ __launch_bounds__(64 * kGlrFwdWaves) void gdr2_glr_fwd_kernel(GlrPara
     constexpr int W = kGlrFwdWaves;
     __shared__ GlrSmem<W> sm;
     const GlrPlace w = glr_place(p, sm);
+    if (w.ord < 0) return;
     const int l = lane_id(), wv = wave_id();
     const long ch = (long)w.strip * kGlrCh + 8 * (l & 7);
     const long t0 = (long)w.ord * kGlrFwdSeg + (wv * 8 + (l >> 3)) * kGlrRun;
@@ -249,6 +258,7 @@ __global__ __launch_bounds__(64 * kGlrBwdWaves) void gdr2_glr_bwd_kernel(GlrPara
     constexpr int W = kGlrBwdWaves;
     __shared__ GlrSmem<W> sm;
     const GlrPlace w = glr_place(p, sm);
+    if (w.ord < 0) return;
     const int l = lane_id(), wv = wave_id();
     const int seg = p.nseg - 1 - w.ord;  // the scan starts at the last segment
     const long ch = (long)w.strip * kGlrCh + 8 * (l & 7);

@@ -382,8 +382,11 @@ gdr2_status gdr2_out_gate_bwd(int64_t rows, int64_t dv, gdr2_dtype dtype, const 
  * conventions at the top of this header hold; x, q, k, v, o, y, h, their gradients and the caches
  * have the caller's dtype, everything else is fp32.  int32 arrays (lengths, positions) live in device
  * memory, 4-byte aligned; their values are not visible to the host checks, so every value has a
- * meaning (below).  NaN and infinities propagate as the formulas say from the rows that are read;
- * rows at and behind a sequence's length are not read, whatever they hold.
+ * meaning (below).  Rows at and behind a sequence's length, and cache slots not written yet, may hold
+ * anything.  A NaN or infinity stays in its row (layer norm; its weight gradients excepted), its
+ * channel (recurrence) or its sequence and key/value head (attention, whose products are formed over
+ * tiles: there it may also reach rows of that sequence that do not see it).  A workspace serves one
+ * call at a time: calls, or captured graphs, that may run at the same time need their own.
  */
 
 /*
@@ -412,14 +415,13 @@ gdr2_status gdr2_layer_norm_bwd(int64_t rows, int64_t D, gdr2_dtype dtype, const
  *     h_t = exp(log_a_t) h_{t-1} + x_t,   h_0 given (NULL = zero)
  * D a multiple of 8 (else GDR2_E_UNSUPPORTED), T >= 0 (T = 0: h_T = h_0, dh_0 = dh_T).
  *   x, h, dh, dx    [B][T][D]  dtype
- *   log_a, dlog_a   [B][T][D]  fp32   (natural log of the decay; any value, -inf forgets exactly)
+ *   log_a, dlog_a   [B][T][D]  fp32   (natural log of the decay, <= 0; -inf forgets exactly)
  *   h0, h_T         [B][D]     fp32 or NULL
  *   workspace       gdr2_glr_fwd_workspace_bytes() bytes; on return its first part holds the state
  *                   entering every 128-token segment, which the backward reads: keep it unchanged
  *                   between the two calls when training
  * The backward, for the cotangents dh of h and dh_T of h_T (NULL = zero), returns dx, dlog_a and dh0
- * (NULL = not wanted); x, log_a as passed to the forward, fwd_workspace the forward's.  Two calls
- * that may run at the same time need workspaces of their own.
+ * (NULL = not wanted); x, log_a as passed to the forward, fwd_workspace the forward's.
  * gdr2_glr_step is one token for N sequences: h_out = exp(log_a) h_in + x (fp32 state, h_in NULL =
  * zero, h_in == h_out allowed), h the same in dtype.
  */

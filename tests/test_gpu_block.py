@@ -174,6 +174,54 @@ def test_swa(dtype, d, B, T, H, Hkv, window, sinks, lengths):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_swa_many_workgroups(dtype, d):
+    """Enough heads for 128 queries and whole query ranges per workgroup, with and without shared heads."""
+    _swa_check(8, 520, 8, 8, d, dtype, 100, 5, [520, 519, 129, 128, 1, 0, 400, 33], seed=13)
+    _swa_check(4, 600, 32, 16, d, dtype, 333, 0, None, seed=14)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_swa_nonfinite_values_stay_in_their_sequence(dtype):
+    """A NaN in one sequence's key/value head reaches neither another sequence nor another head."""
+    q, k, v, dO = _swa_inputs(2, 200, 4, 2, 64, dtype, 15)
+    ref = None
+    for bad in (False, True):
+        if bad:
+            k[0, 50, 1] = float("nan")
+            v[0, 60, 1] = float("inf")
+            dO[0, 70, 2:] = float("nan")
+        qd, kd, vd, gd = dev(q, k, v, dO)
+        o, lse = g2.gdr2_swa_fwd(qd, kd, vd, 64, sinks=1)
+        g = g2.gdr2_swa_bwd(qd, kd, vd, o, lse, gd, 64, sinks=1)
+        out = [o[1], o[0, :, :2], lse[1], lse[0, :2], g["dq"][1], g["dq"][0, :, :2], g["dk"][1], g["dk"][0, :, 0], g["dv"][1],
+               g["dv"][0, :, 0]]
+        if ref is None:
+            ref = out
+        else:
+            assert torch.isnan(o[0, 60:, 2:]).any()
+            for a, b in zip(out, ref):
+                assert torch.equal(a, b)
+
+
+def test_rows_and_channels_are_isolated():
+    x = torch.randn(40, 200, device=DEV)
+    x[7, 3] = float("nan")
+    w = torch.ones(200, device=DEV)
+    y, mean, rstd = g2.gdr2_layer_norm_fwd(x, w)
+    dx = g2.gdr2_layer_norm_bwd(x, w, mean, rstd, torch.ones_like(x))["dx"]
+    for t in (y, dx):
+        assert torch.isnan(t[7]).all() and torch.isfinite(t[torch.arange(40) != 7]).all()
+    x, la = torch.randn(1, 5000, 64, device=DEV), -torch.rand(1, 5000, 64, device=DEV)
+    x[0, 700, 9] = float("nan")
+    h, hT, ws = g2.gdr2_glr_fwd(x, la)
+    g = g2.gdr2_glr_bwd(x, la, torch.ones_like(x), ws)
+    others = torch.arange(64) != 9
+    assert torch.isnan(h[0, 700:, 9]).all() and torch.isfinite(h[0, :700, 9]).all() and torch.isfinite(h[..., others]).all()
+    assert torch.isfinite(g["dx"]).all() and torch.isfinite(g["dlog_a"][..., others]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_swa_many_sink_pieces(dtype):
     """Queries far behind the window: several pieces of the sinks' gradients, the last one ragged."""
     _swa_check(1, 3000, 2, 1, 64, dtype, 33, 40, None, seed=3)
