@@ -87,7 +87,10 @@ struct SwaCut {
     int splits, part_rows, pieces, far0, piece_len;
 };
 // Workgroups of 128 keys fill the card once there are as many as compute units (256); with fewer, the
-// queries of a tile are cut into up to eight parts of at least two tiles of 64.  Pieces of the far
+// queries of a tile are cut into up to eight parts of at least two tiles of 64, two workgroups per unit.
+// Backward in us uncut / up to four / eight / sixteen parts: T=2048 H=16/4 d=128 window 2048 bf16 356 / 155 / 152 /
+// 182, T=512 H=8/2 d=64 70 / 34 / 28 / 29, B=2 T=777 H=6/2 d=64 fp32 202 / 88 / 75 / 76; cut at 256 workgroups
+// too: T=4096 H=8 d=128 162 -> 195.  Pieces of the far
 // queries: up to two workgroups per compute unit, at least 128 queries and at most 64 pieces each.
 inline SwaCut swa_cut(long B, long T, long H, long Hkv, long window, int sinks) {
     SwaCut c{1, 0, 0, 0, 0};

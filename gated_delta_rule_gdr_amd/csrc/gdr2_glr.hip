@@ -10,6 +10,9 @@
 // a segment (kGlrFwdSeg or kGlrBwdSeg tokens) of kGlrCh channels.  Everything is held in fp32.
 //
 // The pass is a stream (9 flops per 8 or more bytes): every element is read once and written once.
+// B=4 T=4096 D=2048 bf16: forward 64 us for 268 MB and the kept states (4.2 TB/s), backward 108 us for 470 MB
+// (4.3 TB/s; it reads x and log_a again), and 5 us each to preset the published words; B=1 T=32749 D=1024 fp32:
+// 91 us (4.4 TB/s) and 137 us (4.9 TB/s).  The step kernel (256 x 2048) takes 3 us, a launch's latency.
 // Segments of one channel strip are joined inside the same launch: a workgroup publishes the map of
 // its segment (A, X in one 64-bit word per channel), then reads the maps before it, at most
 // kGlrGroup of them behind the last published running state, and folds them in their order, so

