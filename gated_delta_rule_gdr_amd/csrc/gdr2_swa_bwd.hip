@@ -17,8 +17,8 @@
 // sums in a fixed order.
 //
 // Bound by the matrix products' issue, and the second kernel also by its registers (dk, dv, k and v of 32
-// keys leave one wave per SIMD).  B=4 T=4096 H=16 d=128 window 2048 bf16: dq 366 us (845 TFLOP/s over its
-// three products), dkv 580 us (711 over its four), reduction 8 us.  Measured there and not kept, for the
+// keys leave one wave per SIMD).  B=4 T=4096 H=16 d=128 window 2048 bf16: dq 339 us (914 TFLOP/s over its
+// three products), dkv 590 us (700 over its four), reduction 8 us.  Measured there and not kept, for the
 // whole backward (953-956 us): dv and dk on different waves, each forming the probabilities, 981; the
 // same with the probabilities handed over through LDS 948, but 87 us instead of 69 at B=3 T=1537 H=12/3
 // d=64; both query blocks of a tile side by side in one wave 1123.

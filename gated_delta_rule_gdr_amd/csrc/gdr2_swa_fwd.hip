@@ -11,10 +11,10 @@
 // alternate 32-key blocks, joined at the end.
 //
 // Bound by the matrix products' issue: two waves per SIMD, one's exponentials beside the other's products.
-// B=4 T=4096 H=16 d=128 window 2048 bf16: 257 us, 803 TFLOP/s over the visible pairs (a library product of
-// 8192^3 random bf16 reaches 1275 on the same card); T=32768, four heads to a key head: 615 us, 867 TFLOP/s.
+// B=4 T=4096 H=16 d=128 window 2048 bf16: 251 us, 823 TFLOP/s over the visible pairs (a library product of
+// 8192^3 random bf16 reaches 1275 on the same card); T=32768, four heads to a key head: 585 us, 911 TFLOP/s.
 // With the work between the products taken out it still needs 193 us.  Measured at the first size and
-// not kept: scores formed one tile ahead of their softmax in the same wave 313 us; 64 queries per wave
+// not kept, against 257 us in the same runs: scores formed one tile ahead of their softmax in the same wave 313 us; 64 queries per wave
 // (one wave per SIMD) 469; two wave groups alternating products and softmax behind barriers 286; three
 // waves per SIMD with 32-key tiles 259.
 #include "gdr2_swa.hpp"
