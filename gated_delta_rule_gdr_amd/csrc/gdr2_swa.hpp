@@ -17,11 +17,12 @@ namespace gdr2 {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 constexpr int kSwaThreads = 256, kSwaWaves = 4;
-// Workgroups of 128 queries: below one per compute unit, 64 queries each and the keys in two halves.
-// T=4096, window 2048, d=128 bf16, forward, us with 128 / 64 queries: 4 heads (128 workgroups) 51 / 38, 8 heads
-// (256) 52 / 50, 12 heads (384) 70 / 85, 16 heads 73 / 89; backward 141 / 121, 151 / 147, -, 260 / 275.
-// B=2 T=777 H=6 d=64 fp32 (84 workgroups): 39 / 22 and 100 / 75.
-constexpr long kSwaNarrowBelow = 256;
+// Workgroups of 128 queries: up to five for four compute units, 64 queries each and the keys in two halves (the
+// busiest unit then has three half shares instead of two whole ones; past that the halves' joining costs more).
+// Window 2048, T=4096, d=128 bf16, forward, us with 128 / 64 queries: 128 workgroups 51 / 38, 256 52 / 50,
+// 288 69 / 59, 320 69 / 67, 384 70 / 85; backward 141 / 121, 151 / 147, 210 / 194, -, -, 512 260 / 275.  Window 512,
+// T=8192, d=64: 256 18 / 19, 320 21 / 18, 448 21 / 24.  B=2 T=777 H=6 d=64 fp32 (84): 39 / 22 and 100 / 75.
+constexpr long kSwaNarrowMost = 320;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.0e38f;
 

@@ -392,7 +392,7 @@ static hipError_t launch_swa_bwd(const SwaParams& p, hipStream_t s) {
     const long heads = (long)p.B * p.H, wide = (p.T + 127) / 128 * heads, narrow = (p.T + 63) / 64 * heads;
     bool done = false;
     if constexpr (Swa<T, D>::NB == 2) {
-        if (wide < kSwaNarrowBelow) {
+        if (wide <= kSwaNarrowMost) {
             hipLaunchKernelGGL((gdr2_swa_dq_kernel<T, D, 2>), dim3((unsigned)narrow), dim3(kSwaThreads), 0, s, p);
             done = true;
         }

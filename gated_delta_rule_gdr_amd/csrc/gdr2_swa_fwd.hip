@@ -7,8 +7,8 @@
 // a score exceeds it by more than 2^8, so the sums stay within fp32 and most tiles rescale nothing.
 // A workgroup takes 128 queries of one head, 32 per wave, and walks the key tiles its queries may
 // see through a double-buffered pair of LDS tiles; grouped heads share the tiles in L2.  Where that
-// gives fewer workgroups than compute units, it takes 64 queries and its two halves (KS = 2) walk
-// alternate 32-key blocks, joined at the end.
+// gives few workgroups for the card (kSwaNarrowMost), it takes 64 queries and its two halves (KS = 2)
+// walk alternate 32-key blocks, joined at the end.
 //
 // Bound by the matrix products' issue: two waves per SIMD, one's exponentials beside the other's products.
 // B=4 T=4096 H=16 d=128 window 2048 bf16: 251 us, 823 TFLOP/s over the visible pairs (a library product of
@@ -149,7 +149,7 @@ template <typename T, int D>
 static hipError_t launch_swa_fwd(const SwaParams& p, hipStream_t s) {
     const long heads = (long)p.B * p.H, wide = (p.T + 127) / 128 * heads, narrow = (p.T + 63) / 64 * heads;
     if constexpr (Swa<T, D>::NB == 2) {
-        if (wide < kSwaNarrowBelow) {
+        if (wide <= kSwaNarrowMost) {
             hipLaunchKernelGGL((gdr2_swa_fwd_kernel<T, D, 2>), dim3((unsigned)narrow), dim3(kSwaThreads), 0, s, p);
             return hipGetLastError();
         }

@@ -182,6 +182,14 @@ def test_swa_many_workgroups(dtype, d):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H", [8, 9])
+def test_swa_padded_grids(dtype, d, H):
+    """320 and 360 workgroups of 128 queries, the two sides of the forward's and dq's split, over a padded batch."""
+    _swa_check(8, 513, H, H, d, dtype, 70, 20, [513, 512, 129, 128, 1, 0, 400, 65], seed=16)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_swa_nonfinite_values_stay_in_their_sequence(dtype):
     """A NaN in one sequence's key/value head reaches neither another sequence nor another head."""
     q, k, v, dO = _swa_inputs(2, 200, 4, 2, 64, dtype, 15)
@@ -311,3 +319,38 @@ def test_decode_steps_continue_a_prefill():
         for n in range(B):
             within(f"o at {i[n]}", o[n], r["o"][n, i[n]], b["o"][n, i[n]])
         pos += 1
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,H,Hkv,window,sinks", [(43, 6, 3, 500, 4), (64, 3, 3, 500, 0), (5, 2, 2, 4000, 10)])
+def test_decode_parts_and_large_positions(dtype, N, H, Hkv, window, sinks):
+    """Caches of which each part of the slots, none, or only the first parts hold anything; positions up to
+    the last int32.  A full cache's slots are all visible, in any order."""
+    d, cap = 64, window + sinks
+    announce(f"decode parts {dtype} N={N} H={H}/{Hkv} window={window} sinks={sinks}")
+    gen = torch.Generator().manual_seed(N)
+    kc, vc = randn(gen, (N, cap, Hkv, d), dtype), randn(gen, (N, cap, Hkv, d), dtype)
+    q, k, v = randn(gen, (N, H, d), dtype), randn(gen, (N, Hkv, d), dtype), randn(gen, (N, Hkv, d), dtype)
+    pos = torch.randint(0, 3 * cap, (N,), generator=gen, dtype=torch.int32)
+    pos[0], pos[1], pos[2], pos[3] = 2 ** 31 - 1, 130, cap - 1, -(2 ** 31)
+    kd, vd, kn, vn, qd, pd = dev(kc, vc, k, v, q, pos)
+    o = g2.gdr2_swa_decode_step(qd, kn, vn, kd, vd, pd, sinks=sinks)
+    torch.cuda.synchronize()
+    for n, p in enumerate(pos.tolist()):
+        if p >= 0:
+            slot = p if p < sinks else sinks + (p - sinks) % window
+            kc[n, slot], vc[n, slot] = k[n], v[n]
+    assert torch.equal(kd.cpu(), kc) and torch.equal(vd.cpu(), vc)
+    for n in (0, 1, 2, 3, N - 1):
+        held = min(int(pos[n]) + 1, cap)
+        if held <= 0:
+            assert not o[n].any()
+            continue
+        K, V, Q = f64(kc[n, :held]), f64(vc[n, :held]), f64(q[n])
+        for h in range(H):
+            Kh, Vh = K[:, h // (H // Hkv)], V[:, h // (H // Hkv)]
+            s = Kh @ Q[h] * d ** -0.5
+            w = np.exp(s - s.max())
+            w /= w.sum()
+            r = dict(smax=float((np.abs(Kh) @ np.abs(Q[h])).max()) * d ** -0.5, o=w @ Vh, o_abs=w @ np.abs(Vh), lse=np.zeros(()))
+            within(f"o[{n}, {h}]", o[n, h], r["o"], swa_bounds(r, dtype, d, cap)["o"])
