@@ -91,7 +91,7 @@ struct SwaBwdWs {
 SwaBwdWs swa_bwd_layout(int64_t B, int64_t T, int64_t H, int64_t Hkv, int64_t d, int64_t window, int64_t sinks) {
     SwaBwdWs w{};
     if (B == 0 || T == 0 || H == 0) return w;
-    w.cut = gdr2::swa_cut(B, T, H, Hkv, window < T ? window : T, (int)sinks);
+    w.cut = gdr2::swa_cut(B, T, H, Hkv, d, window < T ? window : T, (int)sinks);
     size_t off = 0;
     auto take = [&](size_t n) { const size_t o = off; off += round_up(n, 256); return o; };
     w.delta = take((size_t)B * H * T * 4);

@@ -87,17 +87,21 @@ struct SwaCut {
     int splits, part_rows, pieces, far0, piece_len;
 };
 // Workgroups of 128 keys fill the card once there are as many as compute units (256); with fewer, the
-// queries of a tile are cut into up to eight parts of at least two tiles of 64, two workgroups per unit.
+// queries of a tile are cut into up to eight parts of at least two tiles of 64, towards the workgroups the
+// card holds: d=64 bf16 two per unit, d=128 one, unless whole parts leave an eighth of the units idle.
 // Backward in us uncut / up to four / eight / sixteen parts: T=2048 H=16/4 d=128 window 2048 bf16 356 / 155 / 152 /
 // 182, T=512 H=8/2 d=64 70 / 34 / 28 / 29, B=2 T=777 H=6/2 d=64 fp32 202 / 88 / 75 / 76; cut at 256 workgroups
-// too: T=4096 H=8 d=128 162 -> 195.  Pieces of the far
-// queries: up to two workgroups per compute unit, at least 128 queries and at most 64 pieces each.
-inline SwaCut swa_cut(long B, long T, long H, long Hkv, long window, int sinks) {
+// too: T=4096 H=8 d=128 162 -> 195.  Towards one / two per unit, T=4096 window 2048 d=128: 4 heads (128
+// workgroups) 119 / 133, 5 heads 153 / 147, 7 heads 155 / 171; T=2048 H=8 window 512 50 / 65; d=64 T=1537 H=12/3 83 / 69.
+// Pieces of the far queries: up to two workgroups per compute unit, at least 128 queries and at most 64
+// pieces each.
+inline SwaCut swa_cut(long B, long T, long H, long Hkv, long d, long window, int sinks) {
     SwaCut c{1, 0, 0, 0, 0};
     const long heads = B * Hkv, jobs = (T + kSwaKeyTile - 1) / kSwaKeyTile * heads;
     const long seen = window + kSwaKeyTile < T ? window + kSwaKeyTile : T, tiles = (seen + 63) / 64 * (H / Hkv);
     if (jobs < 256) {
-        const long want = 512 / jobs, s = want < tiles / 2 ? want : tiles / 2;
+        const long one = 256 / jobs, want = d == 128 && one * jobs >= 224 ? one : 512 / jobs;
+        const long s = want < tiles / 2 ? want : tiles / 2;
         c.splits = (int)(s < 1 ? 1 : s < 8 ? s : 8);
     }
     const long far0 = (kSwaKeyTile - 1 + window + 63) / 64 * 64;
