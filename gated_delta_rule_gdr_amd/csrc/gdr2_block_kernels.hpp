@@ -93,8 +93,9 @@ struct SwaCut {
 // 182, T=512 H=8/2 d=64 70 / 34 / 28 / 29, B=2 T=777 H=6/2 d=64 fp32 202 / 88 / 75 / 76; cut at 256 workgroups
 // too: T=4096 H=8 d=128 162 -> 195.  Towards one / two per unit, T=4096 window 2048 d=128: 4 heads (128
 // workgroups) 119 / 133, 5 heads 153 / 147, 7 heads 155 / 171; T=2048 H=8 window 512 50 / 65; d=64 T=1537 H=12/3 83 / 69.
-// Pieces of the far queries: up to two workgroups per compute unit, at least 128 queries and at most 64
-// pieces each.
+// Pieces of the far queries: up to one workgroup per two compute units, at least 128 queries and at most 64
+// pieces per head (us with 64 / 128 / 256 / 512 workgroups: B=4 T=4096 H=16 d=128 window 2048 947 / 949 / 954 / 959,
+// T=8192 H=8 window 1024 195 / 189 / 190 / 202, T=16384 H=16/4 window 2048 1254 / 1196 / 1188 / 1187).
 inline SwaCut swa_cut(long B, long T, long H, long Hkv, long d, long window, int sinks) {
     SwaCut c{1, 0, 0, 0, 0};
     const long heads = B * Hkv, jobs = (T + kSwaKeyTile - 1) / kSwaKeyTile * heads;
@@ -107,7 +108,7 @@ inline SwaCut swa_cut(long B, long T, long H, long Hkv, long d, long window, int
     const long far0 = (kSwaKeyTile - 1 + window + 63) / 64 * 64;
     c.far0 = (int)far0;
     if (sinks > 0 && T > far0) {
-        const long want = heads < 512 ? 512 / heads : 1, most = (T - far0 + 127) / 128;
+        const long want = heads < 128 ? 128 / heads : 1, most = (T - far0 + 127) / 128;
         long n = want < most ? want : most;
         n = n < 64 ? n : 64;
         c.piece_len = (int)(((T - far0 + n - 1) / n + 63) / 64 * 64);
