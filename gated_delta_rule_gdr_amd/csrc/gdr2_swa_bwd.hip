@@ -45,7 +45,8 @@ __global__ __launch_bounds__(kSwaThreads, sizeof(T) * D > 256 ? 1 : 2) void gdr2
     const int l = lane_id(), wv = uniform_wave(), n = l & 31, h = l >> 5;
     const int nqt = (int)((p.T + BQ - 1) / BQ);
     const int work = xcd_swizzle(blockIdx.x, gridDim.x);
-    const int qt = work % nqt, bh = work / nqt, b = bh / p.H, hd = bh % p.H, kvh = hd / (p.H / p.Hkv);
+    // a head's last queries first, as in the forward (B=4 T=1500 H=12 d=128 window 2048: backward 208 -> 191 us)
+    const int qt = nqt - 1 - work % nqt, bh = work / nqt, b = bh / p.H, hd = bh % p.H, kvh = hd / (p.H / p.Hkv);
     const int L = swa_length(p, b);
     const int Q0 = qt * BQ, q0 = Q0 + 32 * (wv % QW), i = q0 + n, ks = wv / QW;
     const long qstr = (long)p.H * D * S::ES, kstr = (long)p.Hkv * D * S::ES;
