@@ -18,7 +18,7 @@
 //
 // Bound by the matrix products' issue, and the second kernel also by its registers (dk, dv, k and v of 32
 // keys leave one wave per SIMD).  B=4 T=4096 H=16 d=128 window 2048 bf16: dq 339 us (914 TFLOP/s over its
-// three products), dkv 590 us (700 over its four), reduction 8 us.  Measured there and not kept, for the
+// three products), dkv 596 us (693 over its four), reduction 5 us.  Measured there and not kept, for the
 // whole backward (953-956 us): dv and dk on different waves, each forming the probabilities, 981; the
 // same with the probabilities handed over through LDS 948, but 87 us instead of 69 at B=3 T=1537 H=12/3
 // d=64; both query blocks of a tile side by side in one wave 1123.
@@ -45,8 +45,7 @@ __global__ __launch_bounds__(kSwaThreads, sizeof(T) * D > 256 ? 1 : 2) void gdr2
     const int l = lane_id(), wv = uniform_wave(), n = l & 31, h = l >> 5;
     const int nqt = (int)((p.T + BQ - 1) / BQ);
     const int work = xcd_swizzle(blockIdx.x, gridDim.x);
-    // a head's last queries first, as in the forward (B=4 T=1500 H=12 d=128 window 2048: backward 208 -> 191 us)
-    const int qt = nqt - 1 - work % nqt, bh = work / nqt, b = bh / p.H, hd = bh % p.H, kvh = hd / (p.H / p.Hkv);
+    const int qt = swa_query_tile(p, work % nqt, nqt), bh = work / nqt, b = bh / p.H, hd = bh % p.H, kvh = hd / (p.H / p.Hkv);
     const int L = swa_length(p, b);
     const int Q0 = qt * BQ, q0 = Q0 + 32 * (wv % QW), i = q0 + n, ks = wv / QW;
     const long qstr = (long)p.H * D * S::ES, kstr = (long)p.Hkv * D * S::ES;

@@ -12,7 +12,7 @@
 //
 // Bound by the matrix products' issue: two waves per SIMD, one's exponentials beside the other's products.
 // B=4 T=4096 H=16 d=128 window 2048 bf16: 251 us, 823 TFLOP/s over the visible pairs (a library product of
-// 8192^3 random bf16 reaches 1275 on the same card); T=32768, four heads to a key head: 585 us, 911 TFLOP/s.
+// 8192^3 random bf16 reaches 1275 on the same card); T=32768, four heads to a key head: 610 us, 874 TFLOP/s.
 // With the work between the products taken out it still needs 193 us.  Measured at the first size and
 // not kept, against 257 us in the same runs: scores formed one tile ahead of their softmax in the same wave 313 us; 64 queries per wave
 // (one wave per SIMD) 469; two wave groups alternating products and softmax behind barriers 286; three
@@ -33,8 +33,7 @@ __global__ __launch_bounds__(kSwaThreads, 2) void gdr2_swa_fwd_kernel(SwaParams 
     const int l = lane_id(), wv = uniform_wave(), n = l & 31, h = l >> 5;
     const int nqt = (int)((p.T + BQ - 1) / BQ);
     const int work = xcd_swizzle(blockIdx.x, gridDim.x);
-    // a head's last queries, which see the most keys, first (B=4 T=1500 H=12 d=128 window 2048: 64 -> 50 us)
-    const int qt = nqt - 1 - work % nqt, bh = work / nqt, b = bh / p.H, hd = bh % p.H, kvh = hd / (p.H / p.Hkv);
+    const int qt = swa_query_tile(p, work % nqt, nqt), bh = work / nqt, b = bh / p.H, hd = bh % p.H, kvh = hd / (p.H / p.Hkv);
     const int L = swa_length(p, b);
     const int Q0 = qt * BQ, q0 = Q0 + 32 * (wv % QW), i = q0 + n, ks = wv / QW;
     const long qstr = (long)p.H * D * S::ES, kstr = (long)p.Hkv * D * S::ES;
