@@ -11,7 +11,7 @@
 
 namespace {
 
-constexpr int64_t kMaxGrid = ((int64_t)1 << 31) - 1;  // workgroups of one launch
+constexpr int64_t kMaxInt = ((int64_t)1 << 31) - 1;   // counts that the kernels hold as ints
 
 bool dtype_ok(gdr2_dtype dt) { return dt == GDR2_F32 || dt == GDR2_BF16; }
 size_t esize(gdr2_dtype dt) { return dt == GDR2_F32 ? 4 : 2; }
@@ -28,18 +28,20 @@ gdr2_status status_of(hipError_t e) { return e == hipSuccess ? GDR2_OK : GDR2_E_
 
 // ------------------------------------------------------------------ layer norm
 gdr2_status check_norm(int64_t rows, int64_t D) {
-    if (rows < 0 || D < 0 || rows > kMaxGrid) return GDR2_E_SHAPE;
+    if (rows < 0 || D < 0 || rows > kMaxInt) return GDR2_E_SHAPE;
     if (D < 8 || D > gdr2::kNormMaxD || D % 8) return GDR2_E_UNSUPPORTED;
     return GDR2_OK;
 }
 
 // ------------------------------------------------------------------ gated linear recurrence
-// Afterwards B * T * D <= 2^50 and the segments of a launch fit a grid.
+// Afterwards B * T * D <= 2^50 and one batch row's segments fit a launch.
 gdr2_status check_glr(int64_t B, int64_t T, int64_t D) {
     if (B < 0 || T < 0 || D < 0 || T > ((int64_t)1 << 37) || D > ((int64_t)1 << 30)) return GDR2_E_SHAPE;
     if (D < 8 || D % 8) return GDR2_E_UNSUPPORTED;
     const int64_t nseg = gdr2::glr_segments(T, gdr2::kGlrBwdSeg), strips = gdr2::glr_strips(D);
-    if (!prod_le(B, strips, kMaxGrid) || !prod_le(B * strips, nseg, kMaxGrid)) return GDR2_E_SHAPE;
+    if (!prod_le(B, strips, kMaxInt) || !prod_le(B * strips, nseg, kMaxInt)) return GDR2_E_SHAPE;
+    // (the backward has up to twice the segments and half the threads)
+    if (!prod_le(strips, gdr2::glr_segments(T, gdr2::kGlrFwdSeg), gdr2::max_workgroups(gdr2::kGlrFwdThreads))) return GDR2_E_SHAPE;
     return GDR2_OK;
 }
 struct GlrWs {
@@ -68,12 +70,14 @@ gdr2_status check_heads(int64_t H, int64_t Hkv, int64_t d, int64_t window, int64
     return GDR2_OK;
 }
 bool scale_ok(float s) { return s > 0.f && s < 1e30f; }
-// Afterwards B * T * H <= 2^38 rows and every grid below fits a launch.
+// Afterwards B * H <= 2^22, B * T * H <= 2^31 rows, and the launches of 256 threads fit: a workgroup per 128 queries or
+// keys of a head, and one per key/value head for the sinks' far queries.  (Only launches of a few hundred such
+// workgroups are cut finer.)
 gdr2_status check_swa(int64_t B, int64_t T, int64_t H, int64_t Hkv, int64_t d, int64_t window, int64_t sinks) {
     const gdr2_status st = check_heads(H, Hkv, d, window, sinks);
     if (st != GDR2_OK) return st;
     if (B < 0 || T < 0 || T > ((int64_t)1 << 30)) return GDR2_E_SHAPE;
-    if (!prod_le(B, H, kMaxGrid) || !prod_le(B * H, (T + 63) / 64 + 64, kMaxGrid / 8)) return GDR2_E_SHAPE;
+    if (!prod_le(B, H, (int64_t)1 << 22) || !prod_le(B * H, (T + 127) / 128 + 1, gdr2::max_workgroups(256))) return GDR2_E_SHAPE;
     return GDR2_OK;
 }
 gdr2::SwaParams swa_params(int64_t B, int64_t T, int64_t H, int64_t Hkv, int64_t d, int64_t window, int64_t sinks,
@@ -100,11 +104,18 @@ SwaBwdWs swa_bwd_layout(int64_t B, int64_t T, int64_t H, int64_t Hkv, int64_t d,
     w.total = off;
     return w;
 }
+// The backward's last launch: four channels of every reduced row per thread.
+gdr2_status check_swa_bwd(int64_t B, int64_t T, int64_t H, int64_t Hkv, int64_t d, int64_t window, int64_t sinks) {
+    const gdr2_status st = check_swa(B, T, H, Hkv, d, window, sinks);
+    if (st != GDR2_OK || B == 0 || T == 0 || H == 0) return st;
+    const int64_t rows = gdr2::swa_cut(B, T, H, Hkv, d, window < T ? window : T, (int)sinks).part_rows;
+    return prod_le(B * Hkv, rows * (d / 4), gdr2::max_workgroups(256) * 256) ? GDR2_OK : GDR2_E_SHAPE;
+}
 gdr2_status check_decode(int64_t N, int64_t H, int64_t Hkv, int64_t d, int64_t window, int64_t sinks) {
     const gdr2_status st = check_heads(H, Hkv, d, window, sinks);
     if (st != GDR2_OK) return st;
     if (N < 0 || window > ((int64_t)1 << 30)) return GDR2_E_SHAPE;
-    // a launch has at most max(512, jobs) workgroups, jobs <= N * H
+    // at most N * H jobs, each a workgroup (512 in parts where there are fewer); launches take whole sequences
     if (!prod_le(N, H, ((int64_t)1 << 30)) || !prod_le(N * Hkv, window + sinks, (int64_t)1 << 33)) return GDR2_E_SHAPE;
     return GDR2_OK;
 }
@@ -229,7 +240,7 @@ gdr2_status gdr2_glr_step(int64_t N, int64_t D, gdr2_dtype dt, const void* x, co
     if (!dtype_ok(dt)) return GDR2_E_DTYPE;
     if (N < 0 || D < 0) return GDR2_E_SHAPE;
     if (D < 8 || D % 8) return GDR2_E_UNSUPPORTED;
-    if (!prod_le(N, D, (int64_t)1 << 40)) return GDR2_E_SHAPE;
+    if (!prod_le(N, D, (int64_t)1 << 34)) return GDR2_E_SHAPE;  // eight per thread of one launch
     if (N == 0) return GDR2_OK;
     if (!x || !log_a || !h_out || !h) return GDR2_E_NULL;
     if (!all_aligned({x, log_a, h_in, h_out, h})) return GDR2_E_ALIGN;
@@ -263,7 +274,7 @@ gdr2_status gdr2_swa_fwd(int64_t B, int64_t T, int64_t H, int64_t Hkv, int64_t d
 
 size_t gdr2_swa_bwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Hkv, int64_t d,
                                     int64_t window, int64_t sinks) {
-    if (check_swa(B, T, H, Hkv, d, window, sinks) != GDR2_OK) return 0;
+    if (check_swa_bwd(B, T, H, Hkv, d, window, sinks) != GDR2_OK) return 0;
     return swa_bwd_layout(B, T, H, Hkv, d, window, sinks).total;
 }
 
@@ -273,7 +284,7 @@ gdr2_status gdr2_swa_bwd(int64_t B, int64_t T, int64_t H, int64_t Hkv, int64_t d
                          const void* dO, void* dq, void* dk, void* dv, void* workspace,
                          size_t workspace_bytes, void* stream) {
     if (!dtype_ok(dt)) return GDR2_E_DTYPE;
-    const gdr2_status st = check_swa(B, T, H, Hkv, d, window, sinks);
+    const gdr2_status st = check_swa_bwd(B, T, H, Hkv, d, window, sinks);
     if (st != GDR2_OK) return st;
     if (!scale_ok(scale)) return GDR2_E_VALUE;
     if (B == 0 || T == 0 || H == 0) return GDR2_OK;

@@ -5,6 +5,10 @@
 
 namespace gdr2 {
 
+// Workgroups of one launch: HIP takes gridDim.x * blockDim.x up to 2^32 - 1.  Problems of more rows,
+// batch rows or sequences than that are cut into several launches.
+inline constexpr long max_workgroups(int threads) { return (((long)1 << 32) - 1) / threads; }
+
 // Layer norm over the last axis: y = (x - mean) rstd weight + bias per row of D channels.
 struct NormParams {
     long rows;
@@ -28,6 +32,7 @@ hipError_t norm_dispatch(int dtype_bf16, bool bwd, const NormParams& p, hipStrea
 constexpr int kGlrFwdSeg = 256, kGlrBwdSeg = 128;  // tokens of a segment: a workgroup's share of the time axis
 constexpr int kGlrCh = 64;      // channels of a workgroup
 constexpr int kGlrGroup = 16;   // segments between two published running states
+constexpr int kGlrFwdThreads = 2 * kGlrFwdSeg, kGlrBwdThreads = 2 * kGlrBwdSeg;  // eight channels of four tokens each
 struct GlrParams {
     int B, nseg, nstrip;
     long T, D;
@@ -48,6 +53,8 @@ struct GlrParams {
 };
 inline __host__ __device__ long glr_segments(long T, int seg) { return T <= 0 ? 1 : (T + seg - 1) / seg; }
 inline long glr_strips(long D) { return (D + kGlrCh - 1) / kGlrCh; }
+// One batch row's segments have to fit a launch; batch rows are cut into launches that use pub and
+// ticket in turn.
 hipError_t glr_dispatch(int dtype_bf16, bool bwd, const GlrParams& p, hipStream_t s);
 struct GlrStepParams {
     long n;               // N * D elements
@@ -128,6 +135,7 @@ struct SwaFillParams {
     const void *k, *v;      // [B][T][Hkv][d]
     void *kc, *vc;
     const int* lengths;
+    long first;             // the launch's first piece of the caches (set by the dispatch)
 };
 hipError_t swa_fill_dispatch(const SwaFillParams& p, hipStream_t s);
 struct SwaDecodeParams {

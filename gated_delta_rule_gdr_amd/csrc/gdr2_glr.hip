@@ -36,6 +36,7 @@ constexpr int kGlrWaveTok = 8 * kGlrRun;
 // (whose threads hold three tensors' tokens instead of two).
 constexpr int kGlrFwdWaves = kGlrFwdSeg / kGlrWaveTok, kGlrBwdWaves = kGlrBwdSeg / kGlrWaveTok;
 static_assert(kGlrFwdSeg % kGlrBwdSeg == 0 && kGlrCh == 64, "segment mapping");
+static_assert(kGlrFwdThreads == 64 * kGlrFwdWaves && kGlrBwdThreads == 64 * kGlrBwdWaves, "threads of a segment");
 constexpr unsigned long long kUnpublished = ~0ull;
 
 typedef float f32x8 __attribute__((ext_vector_type(8)));
@@ -211,7 +212,7 @@ __device__ __forceinline__ void glr_load(const GlrParams& p, bool live, long t0,
 }
 
 template <typename T>
-__global__ __launch_bounds__(64 * kGlrFwdWaves) void gdr2_glr_fwd_kernel(GlrParams p) {
+__global__ __launch_bounds__(kGlrFwdThreads) void gdr2_glr_fwd_kernel(GlrParams p) {
     constexpr int W = kGlrFwdWaves;
     __shared__ GlrSmem<W> sm;
     const GlrPlace w = glr_place(p, sm);
@@ -257,7 +258,7 @@ __global__ __launch_bounds__(64 * kGlrFwdWaves) void gdr2_glr_fwd_kernel(GlrPara
 }
 
 template <typename T>
-__global__ __launch_bounds__(64 * kGlrBwdWaves) void gdr2_glr_bwd_kernel(GlrParams p) {
+__global__ __launch_bounds__(kGlrBwdThreads) void gdr2_glr_bwd_kernel(GlrParams p) {
     constexpr int W = kGlrBwdWaves;
     __shared__ GlrSmem<W> sm;
     const GlrPlace w = glr_place(p, sm);
@@ -353,17 +354,41 @@ __global__ __launch_bounds__(256) void gdr2_glr_step_kernel(GlrStepParams p) {
 
 template <typename T>
 static hipError_t launch_glr(bool bwd, const GlrParams& p, hipStream_t s) {
-    if (p.nseg > 1) {
-        const long n = (long)p.B * (p.nseg + p.nseg / kGlrGroup) * p.nstrip * kGlrCh;
-        const long nb = (n + 1023) / 1024;
-        hipLaunchKernelGGL(gdr2_glr_clear_kernel, dim3(nb < 2048 ? nb : 2048), dim3(256), 0, s, p.pub, n, p.ticket);
+    const long row = (long)p.nseg * p.nstrip, fit = max_workgroups(bwd ? kGlrBwdThreads : kGlrFwdThreads) / row;
+    const long most = fit < p.B ? fit : p.B;  // batch rows of a launch
+    if (most < 1) return hipErrorInvalidConfiguration;
+    for (long b0 = 0; b0 < p.B; b0 += most) {
+        GlrParams c = p;
+        const long tok = b0 * p.T * p.D, st = b0 * p.D;
+        c.B = (int)(p.B - b0 < most ? p.B - b0 : most);
+        c.x = (const T*)p.x + tok;
+        c.la = p.la + tok;
+        c.states = p.states + b0 * glr_segments(p.T, kGlrBwdSeg) * p.D;
+        if (bwd) {
+            c.dh = (const T*)p.dh + tok;
+            c.dx = (T*)p.dx + tok;
+            c.dla = p.dla + tok;
+            if (p.dhT) c.dhT = p.dhT + st;
+            if (p.dh0) c.dh0 = p.dh0 + st;
+        } else {
+            c.h = (T*)p.h + tok;
+            if (p.h0) c.h0 = p.h0 + st;
+            if (p.hT) c.hT = p.hT + st;
+        }
+        if (c.nseg > 1) {
+            const long n = (long)c.B * (c.nseg + c.nseg / kGlrGroup) * c.nstrip * kGlrCh;
+            const long nb = (n + 1023) / 1024;
+            hipLaunchKernelGGL(gdr2_glr_clear_kernel, dim3(nb < 2048 ? nb : 2048), dim3(256), 0, s, c.pub, n, c.ticket);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+        const dim3 grid((unsigned)(c.B * row));
+        if (bwd) hipLaunchKernelGGL((gdr2_glr_bwd_kernel<T>), grid, dim3(kGlrBwdThreads), 0, s, c);
+        else hipLaunchKernelGGL((gdr2_glr_fwd_kernel<T>), grid, dim3(kGlrFwdThreads), 0, s, c);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    const dim3 grid((unsigned)((long)p.B * p.nseg * p.nstrip));
-    if (bwd) hipLaunchKernelGGL((gdr2_glr_bwd_kernel<T>), grid, dim3(64 * kGlrBwdWaves), 0, s, p);
-    else hipLaunchKernelGGL((gdr2_glr_fwd_kernel<T>), grid, dim3(64 * kGlrFwdWaves), 0, s, p);
-    return hipGetLastError();
+    return hipSuccess;
 }
 
 hipError_t glr_dispatch(int bf, bool bwd, const GlrParams& p, hipStream_t s) {

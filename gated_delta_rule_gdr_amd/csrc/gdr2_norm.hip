@@ -293,10 +293,20 @@ static hipError_t launch_norm(bool bwd, const NormParams& p, hipStream_t s) {
         constexpr int NV = decltype(nv)::value, LPR = decltype(lpr)::value, WPR = decltype(wpr)::value;
         constexpr int R = RowMap<LPR, WPR>::kRows;
         if (!bwd) {
-            if (p.rows == 0) return hipSuccess;
-            hipLaunchKernelGGL((gdr2_norm_fwd_kernel<T, NV, LPR, WPR>), dim3((p.rows + R - 1) / R),
-                               dim3(kNormThreads), 0, s, p);
-            return hipGetLastError();
+            const long most = max_workgroups(kNormThreads) * R;
+            for (long r0 = 0; r0 < p.rows; r0 += most) {
+                NormParams c = p;
+                c.rows = p.rows - r0 < most ? p.rows - r0 : most;
+                c.x = (const T*)p.x + r0 * p.D;
+                c.y = (T*)p.y + r0 * p.D;
+                if (p.mean) c.mean = p.mean + r0;
+                if (p.rstd) c.rstd = p.rstd + r0;
+                hipLaunchKernelGGL((gdr2_norm_fwd_kernel<T, NV, LPR, WPR>), dim3((unsigned)((c.rows + R - 1) / R)),
+                                   dim3(kNormThreads), 0, s, c);
+                const hipError_t e = hipGetLastError();
+                if (e != hipSuccess) return e;
+            }
+            return hipSuccess;
         }
         const long nb = norm_bwd_blocks(p.rows, p.D);
         if (nb > 0) {

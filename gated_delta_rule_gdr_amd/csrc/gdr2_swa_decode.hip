@@ -228,11 +228,25 @@ int swa_decode_splits(long N, long Hkv, long groups, long slots) {
 
 template <typename T, int D>
 static hipError_t launch_decode(const SwaDecodeParams& p, hipStream_t s) {
-    const int groups = (p.H / p.Hkv + kDecHeads - 1) / kDecHeads;
-    const long jobs = (long)p.N * p.Hkv * groups;
-    hipLaunchKernelGGL((gdr2_swa_decode_kernel<T, D>), dim3((unsigned)(jobs * p.splits)), dim3(kDecThreads), 0, s, p);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.splits == 1) return e;
+    const long per = (long)p.Hkv * ((p.H / p.Hkv + kDecHeads - 1) / kDecHeads);  // workgroups of a sequence's part
+    const long fit = max_workgroups(kDecThreads) / (per * p.splits), most = fit < p.N ? fit : p.N;
+    if (most < 1 || (p.splits > 1 && most < p.N)) return hipErrorInvalidConfiguration;  // parts: few jobs only
+    for (long n0 = 0; n0 < p.N; n0 += most) {
+        SwaDecodeParams c = p;
+        const long row = D * (long)sizeof(T), kv = n0 * p.Hkv * row;
+        c.N = (int)(p.N - n0 < most ? p.N - n0 : most);
+        c.q = (const char*)p.q + n0 * p.H * row;
+        c.o = (char*)p.o + n0 * p.H * row;
+        c.k = (const char*)p.k + kv;
+        c.v = (const char*)p.v + kv;
+        c.kc = (char*)p.kc + kv * (p.window + p.sinks);
+        c.vc = (char*)p.vc + kv * (p.window + p.sinks);
+        c.pos = p.pos + n0;
+        hipLaunchKernelGGL((gdr2_swa_decode_kernel<T, D>), dim3((unsigned)(c.N * per * p.splits)), dim3(kDecThreads), 0, s, c);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    if (p.splits == 1) return hipSuccess;
     hipLaunchKernelGGL((gdr2_swa_decode_join_kernel<T, D>), dim3((unsigned)((long)p.N * p.H)), dim3(kDecThreads), 0, s, p);
     return hipGetLastError();
 }
@@ -245,7 +259,7 @@ hipError_t swa_decode_dispatch(int bf, const SwaDecodeParams& p, hipStream_t s) 
 // One 16-byte piece of a slot per thread, keys and values: the newest position below the length that
 // lives in the slot; a slot none lives in keeps its contents.
 __global__ __launch_bounds__(256) void gdr2_swa_fill_kernel(SwaFillParams p) {
-    const long slots = p.window + p.sinks, x = (long)blockIdx.x * 256 + threadIdx.x;
+    const long slots = p.window + p.sinks, x = p.first + (long)blockIdx.x * 256 + threadIdx.x;
     if (x >= p.B * slots * p.row16) return;
     const long piece = x % p.row16, slot = x / p.row16 % slots, b = x / p.row16 / slots;
     long L = p.lengths ? p.lengths[b] : p.T;
@@ -259,9 +273,16 @@ __global__ __launch_bounds__(256) void gdr2_swa_fill_kernel(SwaFillParams p) {
 }
 
 hipError_t swa_fill_dispatch(const SwaFillParams& p, hipStream_t s) {
-    const long n = p.B * (p.window + p.sinks) * p.row16;
-    hipLaunchKernelGGL(gdr2_swa_fill_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, p);
-    return hipGetLastError();
+    const long n = p.B * (p.window + p.sinks) * p.row16, most = max_workgroups(256) * 256;
+    for (long first = 0; first < n; first += most) {
+        SwaFillParams c = p;
+        c.first = first;
+        const long m = n - first < most ? n - first : most;
+        hipLaunchKernelGGL(gdr2_swa_fill_kernel, dim3((unsigned)((m + 255) / 256)), dim3(256), 0, s, c);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace gdr2

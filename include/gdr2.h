@@ -413,7 +413,8 @@ gdr2_status gdr2_layer_norm_bwd(int64_t rows, int64_t D, gdr2_dtype dtype, const
 /*
  * Elementwise gated linear recurrence, per batch row and channel:
  *     h_t = exp(log_a_t) h_{t-1} + x_t,   h_0 given (NULL = zero)
- * D a multiple of 8 (else GDR2_E_UNSUPPORTED), T >= 0 (T = 0: h_T = h_0, dh_0 = dh_T).
+ * D a multiple of 8 (else GDR2_E_UNSUPPORTED), T >= 0 (T = 0: h_T = h_0, dh_0 = dh_T); with s = ceil(D / 64):
+ * s ceil(T / 256) < 2^23 and B s ceil(T / 128) < 2^31, gdr2_glr_step N * D <= 2^34 (else GDR2_E_SHAPE).
  *   x, h, dh, dx    [B][T][D]  dtype
  *   log_a, dlog_a   [B][T][D]  fp32   (natural log of the decay, <= 0; -inf forgets exactly)
  *   h0, h_T         [B][D]     fp32 or NULL
@@ -442,7 +443,8 @@ gdr2_status gdr2_glr_step(int64_t N, int64_t D, gdr2_dtype dtype, const void* x,
  * Causal sliding-window attention whose first `sinks` tokens stay visible.  Query i of a sequence of
  * L tokens sees key j when j <= i < L and (i - j < window or j < sinks):
  *     o_i = sum_j softmax_j(scale q_i . k_j) v_j,   lse_i = log sum_j exp(scale q_i . k_j)
- * Query head h reads key/value head h / (H / Hkv); H must be a multiple of Hkv (else GDR2_E_SHAPE).
+ * Query head h reads key/value head h / (H / Hkv); H must be a multiple of Hkv, H <= 32768, T <= 2^30, B * H <= 2^22 and
+ * B * H * (ceil(T / 128) + 1) < 2^24 (else GDR2_E_SHAPE; the backward with sinks also B * Hkv * d < 2^28).
  *   q, o, dO, dq    [B][T][H][d]    dtype       d in {64, 128}
  *   k, v, dk, dv    [B][T][Hkv][d]  dtype
  *   lengths         [B] int32 or NULL (every sequence has T tokens); values are clamped to [0, T].
@@ -465,7 +467,8 @@ gdr2_status gdr2_swa_bwd(int64_t B, int64_t T, int64_t H, int64_t Hkv, int64_t d
 /*
  * The bounded cache of that attention for decoding: [N][sinks + window][Hkv][d] per keys and values.
  * Position p lives in slot p (p < sinks) or sinks + (p - sinks) mod window, so a sequence of any
- * length needs window + sinks rows.
+ * length needs window + sinks rows.  window <= 2^30, N * H <= 2^30 and N * Hkv * (window + sinks) <= 2^33 (else
+ * GDR2_E_SHAPE); gdr2_swa_cache_fill takes B, T and Hkv within the attention's limits.
  * gdr2_swa_cache_fill stores, from a prefill's k and v ([B][T][Hkv][d]), the positions a token at
  * position L (the length) may still see into their slots; other slots are left as they were.
  * gdr2_swa_decode_step stores the new token's k and v ([N][Hkv][d]) at position pos[n] into the cache

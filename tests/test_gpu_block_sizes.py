@@ -1,0 +1,97 @@
+"""Problems that take more than one launch (HIP counts a launch in work items, below 2^32): rows on both
+sides of a cut equal those of a small call bit for bit."""
+import pytest
+import torch
+
+import gated_delta_rule_gdr_amd as g2
+from tests._util import announce
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+MAX_ITEMS = (1 << 32) - 1
+
+
+def _room(nbytes):
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < nbytes:
+        pytest.skip(f"needs {nbytes >> 30} GiB of device memory")
+
+
+def test_layer_norm_rows_beyond_a_launch():
+    """8 channels: 64 rows per workgroup of 512 threads, a launch takes (2^32 - 1) // 512 workgroups."""
+    D, cut = 8, MAX_ITEMS // 512 * 64
+    rows = cut + 4099
+    announce(f"layer norm rows={rows} D={D}")
+    _room(24 << 30)
+    x = torch.randn(rows, D, device=DEV, dtype=torch.bfloat16)
+    w, b = torch.randn(D, device=DEV), torch.randn(D, device=DEV)
+    y, mean, rstd = g2.gdr2_layer_norm_fwd(x, w, b)
+    for at in (0, cut - 2000, rows - 4000):
+        s = slice(at, at + 4000)
+        for got, want in zip((y[s], mean[s], rstd[s]), g2.gdr2_layer_norm_fwd(x[s].contiguous(), w, b)):
+            assert torch.equal(got, want), at
+
+
+@pytest.mark.parametrize("T", [1, 300])
+def test_recurrence_batch_beyond_a_launch(T):
+    """One channel strip per batch row: a forward launch takes (2^32 - 1) // 512 segments of 256 tokens,
+    a backward launch (2^32 - 1) // 256 of 128."""
+    D, nf, nb = 8, (T + 255) // 256, (T + 127) // 128
+    cf, cb = MAX_ITEMS // 512 // nf, MAX_ITEMS // 256 // nb
+    B = (cb if T == 1 else cf) + 77   # (T = 300: the forward alone is cut; its tensors take 80 GB)
+    announce(f"recurrence B={B} T={T} D={D}")
+    _room(100 << 30)
+    x = torch.randn(B, T, D, device=DEV, dtype=torch.bfloat16)
+    la = torch.rand(B, T, D, device=DEV).neg_()
+    h0 = torch.randn(B, D, device=DEV)
+    h, hT, ws = g2.gdr2_glr_fwd(x, la, h0)
+    g = g2.gdr2_glr_bwd(x, la, x, ws, h0) if T == 1 else None
+    for at in (0, cf - 50, B - 100):
+        s = slice(at, at + 100)
+        sx, sl, s0 = x[s].contiguous(), la[s].contiguous(), h0[s].contiguous()
+        rh, rT, rws = g2.gdr2_glr_fwd(sx, sl, s0)
+        assert torch.equal(h[s], rh) and torch.equal(hT[s], rT), at
+        if g:
+            r = g2.gdr2_glr_bwd(sx, sl, sx, rws, s0)
+            for n in r:
+                assert torch.equal(g[n][s], r[n]), (n, at)
+
+
+def test_decode_sequences_beyond_a_launch():
+    """One workgroup of 256 threads per sequence and key/value head."""
+    N, d, W = MAX_ITEMS // 256 + 77, 64, 2
+    announce(f"decode N={N}")
+    _room(40 << 30)
+    q, k, v = (torch.randn(N, 1, d, device=DEV, dtype=torch.bfloat16) for _ in range(3))
+    kc = torch.randn(N, W, 1, d, device=DEV, dtype=torch.bfloat16)
+    vc = torch.randn(N, W, 1, d, device=DEV, dtype=torch.bfloat16)
+    pos = (torch.arange(N, device=DEV, dtype=torch.int32) % 5) - 1
+    # 200 sequences around each place, before the call stores its tokens
+    small = {at: [t[at:at + 200].clone() for t in (q, k, v, kc, vc, pos)] for at in (0, N - 200, MAX_ITEMS // 256 - 100)}
+    o = g2.gdr2_swa_decode_step(q, k, v, kc, vc, pos)
+    for at, s in small.items():
+        want = g2.gdr2_swa_decode_step(*s)
+        assert torch.equal(o[at:at + 200], want) and torch.equal(kc[at:at + 200], s[3]) and torch.equal(vc[at:at + 200], s[4]), at
+
+
+def test_cache_fill_beyond_a_launch():
+    """Caches of more than 64 GiB: one thread per 16 bytes.  Only the slots of 100 tokens per sequence are
+    written, so the rest of the memory is never touched."""
+    B, T, Hkv, d, W = 1100, 100, 8, 128, 32768
+    assert B * W * Hkv * d * 2 // 16 > MAX_ITEMS
+    announce(f"cache fill B={B} window={W}")
+    _room(152 << 30)
+    kc = torch.empty(B, W, Hkv, d, device=DEV, dtype=torch.bfloat16)
+    vc = torch.empty_like(kc)
+    k = torch.randn(B, T, Hkv, d, device=DEV, dtype=torch.bfloat16)
+    v = torch.randn(B, T, Hkv, d, device=DEV, dtype=torch.bfloat16)
+    kc[:, T] = 1.0
+    vc[:, T] = 2.0
+    lengths = torch.full((B,), T, device=DEV, dtype=torch.int32)
+    lengths[-2], lengths[-1] = 0, T - 1
+    kc[-2:, :T], vc[-2:, :T] = 3.0, 4.0
+    g2.gdr2_swa_cache_fill(k, v, kc, vc, lengths=lengths)
+    assert torch.equal(kc[:-2, :T], k[:-2]) and torch.equal(vc[:-2, :T], v[:-2])
+    assert (kc[:, T] == 1.0).all() and (vc[:, T] == 2.0).all()
+    assert (kc[-2, :T] == 3.0).all() and (vc[-2, :T] == 4.0).all()
+    assert torch.equal(kc[-1, :T - 1], k[-1, :T - 1]) and (kc[-1, T - 1] == 3.0).all() and (vc[-1, T - 1] == 4.0).all()
