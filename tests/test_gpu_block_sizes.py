@@ -1,5 +1,6 @@
-"""Problems that take more than one launch (HIP counts a launch in work items, below 2^32): rows on both
-sides of a cut equal those of a small call bit for bit."""
+"""Large problems.  Those that take more than one launch (HIP counts a launch in work items, below 2^32):
+rows on both sides of a cut equal those of a small call bit for bit.  Long sums: the rounding of a scan
+grows with its groups, not with its segments."""
 import pytest
 import torch
 
@@ -95,3 +96,31 @@ def test_cache_fill_beyond_a_launch():
     assert (kc[:, T] == 1.0).all() and (vc[:, T] == 2.0).all()
     assert (kc[-2, :T] == 3.0).all() and (vc[-2, :T] == 4.0).all()
     assert torch.equal(kc[-1, :T - 1], k[-1, :T - 1]) and (kc[-1, T - 1] == 3.0).all() and (vc[-1, T - 1] == 4.0).all()
+
+
+def test_recurrence_rounds_once_per_group():
+    """Nothing decays and every term is positive, so the relative error of a state is at most half a step
+    (2^-24) per rounding on its way: 4 in a thread's run, 3 in the wave's scan, one per wave of the segment (8
+    forward, 4 backward), 16 in a group's composition, one per group of 16 segments (of 256 / 128 tokens),
+    and 8 where the state enters the segment, the wave and the run.  Rounding once per segment instead adds
+    up to one per segment: 127 half steps were measured forward with these terms, above the 71 allowed."""
+    T, D = 1 << 17, 64
+    gen = torch.Generator().manual_seed(61)
+    c, u = 1.0 + torch.rand(D, generator=gen), 1.0 + torch.rand(D, generator=gen)
+    announce(f"recurrence of {T} equal terms")
+    x, dh = (v.to(DEV).expand(1, T, D).contiguous() for v in (c, u))
+    la = torch.zeros(1, T, D, device=DEV)
+    h, hT, ws = g2.gdr2_glr_fwd(x, la)
+    g = g2.gdr2_glr_bwd(x, la, dh, ws)
+    t = torch.arange(1, T + 1, dtype=torch.float64, device=DEV)[:, None]
+    c, u = c.double().to(DEV), u.double().to(DEV)
+    nf, nb = (4 + 3 + w + 16 + T // (16 * s) + 8 for w, s in ((8, 256), (4, 128)))
+    step = 2.0 ** -24 * 1.0001   # (terms of second order: 100 half steps of 2^-24)
+    H, G = t * c, (T + 1 - t) * u
+    assert ((h[0].double() - H).abs() <= nf * step * H).all()
+    assert ((hT[0].double() - H[-1]).abs() <= nf * step * H[-1]).all()
+    assert ((g["dx"][0].double() - G).abs() <= nb * step * G).all()
+    assert ((g["dh0"][0].double() - G[0]).abs() <= nb * step * G[0]).all()
+    # R_t h_{t-1}: the state rebuilt from the one that enters the segment of 128
+    P = G * (H - c)
+    assert ((g["dlog_a"][0].double() - P).abs() <= (nf + nb + 16) * step * P).all()
