@@ -75,7 +75,8 @@ __device__ __forceinline__ void publish(unsigned long long* p, unsigned long lon
     __hip_atomic_store(p, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 // Waits of a call that has its workspace to itself end within microseconds.  The bound (some tenths of a
-// second) is for a workspace that another call clears meanwhile: such calls return NaN, not never.
+// second) is for a workspace that another call uses meanwhile, which the interface forbids: such calls end, and
+// what they and the other call leave in their outputs and in the workspace is undefined.
 constexpr int kAwaitPolls = 1 << 18;
 __device__ __forceinline__ unsigned long long await(unsigned long long* p) {
     unsigned long long w = kUnpublished;
@@ -84,7 +85,7 @@ __device__ __forceinline__ unsigned long long await(unsigned long long* p) {
         if (w != kUnpublished) break;
         __builtin_amdgcn_s_sleep(2);
     }
-    return w;  // (kUnpublished reads as a pair of NaN)
+    return w;
 }
 
 template <int W>
@@ -97,7 +98,7 @@ struct GlrSmem {
 
 // Where the workgroup stands in the scan: its place `ord` (0 = first segment of the scan), strip
 // and batch row.  Tickets count the strips of one place before the next place.  One behind the last
-// (again: a workspace that another call uses) is nobody's: ord < 0.
+// (again: a workspace that another call uses) is nobody's: ord < 0, and its workgroup writes nothing.
 struct GlrPlace {
     int ord, strip, b;
 };

@@ -386,7 +386,8 @@ gdr2_status gdr2_out_gate_bwd(int64_t rows, int64_t dv, gdr2_dtype dtype, const 
  * anything.  A NaN or infinity stays in its row (layer norm; its weight gradients excepted), its
  * channel (recurrence) or its sequence and key/value head (attention, whose products are formed over
  * tiles: there it may also reach rows of that sequence that do not see it).  A workspace serves one
- * call at a time: calls, or captured graphs, that may run at the same time need their own.
+ * call at a time: calls, or captured graphs, that may run at the same time need their own (with a shared one
+ * they end, but their outputs are undefined).
  */
 
 /*
