@@ -1,8 +1,9 @@
 // The launches that libgdr2.so makes for the operators around the mixer, seen from a host without a GPU:
 // this program defines the runtime's launch and registration entry points itself, so the library,
 // loaded as built, hands every launch to the checks below and nothing runs.  Checked of each launch:
-// HIP's limit of 2^32 - 1 work items, and per operator that the launches of one call cover the
-// problem once, in order.
+// HIP's limit of 2^32 - 1 work items, per operator that the launches of one call cover the problem
+// once, in order, and that all a launch's grid writes of the workspace lies in what the size query
+// returned (each kernel's needs are counted here from its grid, apart from the library's layouts).
 #include <dlfcn.h>
 
 #include <cstdint>
@@ -92,6 +93,17 @@ static std::string text(const char* f, std::initializer_list<int64_t> v) {
     return s;
 }
 
+static uintptr_t g_ws, g_ws_end;  // the workspace of the running call: W(i, queried bytes)
+static void* W(int i, size_t n) {
+    g_ws = (uintptr_t)A(i);
+    g_ws_end = g_ws + n;
+    return A(i);
+}
+static bool inside(const void* p, int64_t n) { return n == 0 || (n > 0 && (uintptr_t)p >= g_ws && (uintptr_t)p + n <= g_ws_end); }
+static bool apart(const void* p, int64_t n, const void* q, int64_t m) {
+    return n == 0 || m == 0 || (uintptr_t)p + n <= (uintptr_t)q || (uintptr_t)q + m <= (uintptr_t)p;
+}
+
 static int64_t g_done;      // rows, batch rows, sequences or pieces covered so far by the call's launches
 static int64_t g_D, g_T, g_es;
 
@@ -119,6 +131,30 @@ static void norm_fwd() {
         }
 }
 
+static int64_t g_parts;
+static void norm_bwd() {
+    for (int64_t D : {8, 64, 72, 128, 256, 512, 1000, 2048, 4096, 8192, 16384})
+        for (int64_t rows : {(int64_t)0, (int64_t)1, (int64_t)63, (int64_t)511, (int64_t)4099, (int64_t)16384, (int64_t)100000, ((int64_t)1 << 31) - 1})
+            for (bool bias : {false, true}) {
+                g_call = text("layer_norm_bwd", {rows, D, bias});
+                const size_t n = LIB(gdr2_layer_norm_bwd_workspace_bytes)(rows, D);
+                g_D = D, g_parts = 0;
+                g_seen = [](const Launch& l) {
+                    const auto& p = params<gdr2::NormParams>(l);
+                    if (is(l, "norm_reduce")) {  // columns of 64, one or two rows of them, over the parts just written
+                        CHECK(*(long*)l.args[1] == g_parts && (int64_t)l.grid.x == (g_D + 63) / 64 && l.grid.y == (p.dbias ? 2 : 1));
+                        return;
+                    }
+                    CHECK(is(l, "norm_bwd") && p.D == g_D && g_parts == 0);
+                    g_parts = l.grid.x;  // every workgroup writes two rows of D sums
+                    CHECK(inside(p.part, g_parts * 2 * g_D * 4));
+                };
+                const long before = g_launches;
+                CHECK(LIB(gdr2_layer_norm_bwd)(rows, D, GDR2_BF16, A(0), F(1), F(2), F(3), A(4), A(5), F(6), bias ? F(7) : nullptr, W(8, n), n, nullptr) == GDR2_OK);
+                CHECK(g_launches == before + (rows ? 2 : 1));
+            }
+}
+
 static void glr() {
     struct Case { int64_t B, T, D; };
     for (Case c : {Case{1, 1, 8}, Case{3, 300, 136}, Case{(int64_t)1 << 23, 1, 8}, Case{((int64_t)1 << 30) + 1, 1, 8}, Case{((int64_t)1 << 20), 256, 1024},
@@ -129,7 +165,11 @@ static void glr() {
             CHECK(f > 0);
             g_done = 0, g_D = c.D, g_T = c.T;
             g_seen = [](const Launch& l) {
-                if (is(l, "glr_clear")) return;
+                if (is(l, "glr_clear")) {  // words and ticket of the launch behind it
+                    CHECK(inside(*(void**)l.args[0], *(long*)l.args[1] * 8) && inside(*(void**)l.args[2], 4));
+                    g_parts = *(long*)l.args[1];
+                    return;
+                }
                 const auto& p = params<gdr2::GlrParams>(l);
                 const bool back = is(l, "glr_bwd");
                 const int64_t seg = back ? 128 : 256, first = g_done * g_T * g_D;
@@ -138,12 +178,21 @@ static void glr() {
                 CHECK((int64_t)l.grid.x == (int64_t)p.B * p.nseg * p.nstrip && l.block.x == 2 * seg);
                 CHECK(p.x == (const char*)A(0) + 2 * first && p.la == F(1) + first);
                 CHECK(p.states == F(5) + g_done * ((g_T + 127) / 128) * g_D);
+                if (p.nseg > 1) {  // one word per segment and channel of a strip, one per 16 whole segments
+                    const int64_t words = (int64_t)p.B * (p.nseg + p.nseg / 16) * p.nstrip * 64;
+                    CHECK(words == g_parts && inside(p.pub, words * 8) && inside(p.ticket, 4) && apart(p.pub, words * 8, p.ticket, 4));
+                }
+                if (!back) {
+                    const int64_t kept = (int64_t)p.B * ((g_T + 127) / 128) * g_D * 4;
+                    CHECK(inside(p.states, kept));
+                    if (p.nseg > 1) CHECK(apart(p.states, kept, p.pub, g_parts * 8) && apart(p.states, kept, p.ticket, 4));
+                }
                 if (back) CHECK(p.dh == (char*)A(3) + 2 * first && p.dhT == F(4) + g_done * g_D && p.dx == (char*)A(6) + 2 * first && p.dla == F(7) + first && p.dh0 == F(8) + g_done * g_D);
                 else CHECK(p.h0 == F(2) + g_done * g_D && p.h == (char*)A(3) + 2 * first && p.hT == F(4) + g_done * g_D);
                 g_done += p.B;
             };
-            if (bwd) CHECK(LIB(gdr2_glr_bwd)(c.B, c.T, c.D, GDR2_BF16, A(0), F(1), A(5), f, A(3), F(4), A(6), F(7), F(8), A(9), n, nullptr) == GDR2_OK);
-            else CHECK(LIB(gdr2_glr_fwd)(c.B, c.T, c.D, GDR2_BF16, A(0), F(1), F(2), A(3), F(4), A(5), f, nullptr) == GDR2_OK);
+            if (bwd) CHECK(LIB(gdr2_glr_bwd)(c.B, c.T, c.D, GDR2_BF16, A(0), F(1), A(5), f, A(3), F(4), A(6), F(7), F(8), W(9, n), n, nullptr) == GDR2_OK);
+            else CHECK(LIB(gdr2_glr_fwd)(c.B, c.T, c.D, GDR2_BF16, A(0), F(1), F(2), A(3), F(4), W(5, f), f, nullptr) == GDR2_OK);
             CHECK(g_done == c.B);
         }
     g_call = "glr: one batch row beyond a launch";
@@ -164,7 +213,8 @@ static void glr() {
 static int64_t g_H, g_Hkv, g_slots;
 static void decode() {
     struct Case { int64_t N, H, Hkv, window, sinks; };
-    for (Case c : {Case{1, 4, 1, 4096, 4}, Case{256, 16, 4, 2048, 4}, Case{(int64_t)1 << 24, 1, 1, 1, 0}, Case{((int64_t)1 << 25) + 7, 4, 2, 1, 3},
+    for (Case c : {Case{1, 4, 1, 4096, 4}, Case{1, 1, 1, 1, 0}, Case{1, 40, 1, 1 << 20, 64}, Case{3, 4, 2, 129, 0}, Case{24, 16, 4, 8192, 0}, Case{40, 8, 4, 8192, 0},
+                   Case{47, 16, 4, 2048, 4}, Case{48, 16, 4, 2048, 4}, Case{64, 16, 4, 2048, 4}, Case{191, 17, 1, 900, 0}, Case{192, 1, 1, 900, 0}, Case{256, 16, 4, 2048, 4}, Case{(int64_t)1 << 24, 1, 1, 1, 0}, Case{((int64_t)1 << 25) + 7, 4, 2, 1, 3},
                    Case{((int64_t)1 << 23) + 1, 34, 2, 2, 0}, Case{(int64_t)1 << 30, 1, 1, 8, 0}}) {
         g_call = text("swa_decode_step", {c.N, c.H, c.Hkv, c.window, c.sinks});
         const size_t n = LIB(gdr2_swa_decode_workspace_bytes)(c.N, c.H, c.Hkv, 64, c.window, c.sinks);
@@ -175,13 +225,15 @@ static void decode() {
                 CHECK(p.splits > 1 && (int64_t)l.grid.x == p.N * g_H);
                 return;
             }
+            // a part: sixteen heads of a row and two statistics, the statistics 16 bytes
+            if (p.splits > 1) CHECK(inside(p.part, (int64_t)l.grid.x * 16 * (64 + 4) * 4));
             const int64_t row = 64 * 2, kv = g_done * g_Hkv * row;
             CHECK(is(l, "swa_decode") && (int64_t)l.grid.x == (int64_t)p.N * g_Hkv * ((g_H / g_Hkv + 15) / 16) * p.splits);
             CHECK(p.q == (char*)A(0) + g_done * g_H * row && p.o == (char*)A(6) + g_done * g_H * row && p.k == (char*)A(1) + kv && p.v == (char*)A(2) + kv);
             CHECK(p.kc == (char*)A(3) + kv * g_slots && p.vc == (char*)A(4) + kv * g_slots && p.pos == (const int*)A(5) + g_done);
             g_done += p.N;
         };
-        CHECK(LIB(gdr2_swa_decode_step)(c.N, c.H, c.Hkv, 64, GDR2_BF16, c.window, c.sinks, 1.f, A(0), A(1), A(2), A(3), A(4), (int32_t*)A(5), A(6), A(7), n, nullptr) == GDR2_OK);
+        CHECK(LIB(gdr2_swa_decode_step)(c.N, c.H, c.Hkv, 64, GDR2_BF16, c.window, c.sinks, 1.f, A(0), A(1), A(2), A(3), A(4), (int32_t*)A(5), A(6), W(7, n), n, nullptr) == GDR2_OK);
         CHECK(g_done == c.N);
     }
 }
@@ -226,6 +278,50 @@ static void attention() {
                     }
 }
 
+// What the backward's launches keep in the workspace, at sizes that cut keys and far queries every way.
+static int64_t g_win, g_sinks, g_B;
+static void attention_parts() {
+    for (int64_t B : {1, 3, 40})
+        for (int64_t T : {1, 63, 128, 129, 777, 1537, 4096, 8192, 32768})
+            for (int64_t Hkv : {1, 3, 16})
+                for (int64_t G : {1, 4})
+                    for (int64_t win : {1, 64, 256, 2048, 1 << 20})
+                        for (int64_t sinks : {0, 1, 33, 64}) {
+                            g_call = text("swa_bwd", {B, T, Hkv * G, Hkv, win, sinks});
+                            g_B = B, g_T = T, g_Hkv = Hkv, g_H = Hkv * G, g_win = win < T ? win : T, g_sinks = sinks, g_parts = 0;
+                            const size_t n = LIB(gdr2_swa_bwd_workspace_bytes)(B, T, g_H, Hkv, 64, win, sinks);
+                            g_seen = [](const Launch& l) {
+                                const auto& p = params<gdr2::SwaParams>(l);
+                                const int64_t bk = g_B * g_Hkv, tiles = (g_T + 127) / 128 * bk, sums = 64 * 4;
+                                CHECK(p.T == g_T && p.window == g_win && p.sinks == g_sinks);
+                                if (is(l, "swa_dq")) {
+                                    const int64_t wide = (g_T + 127) / 128 * g_B * g_H, narrow = (g_T + 63) / 64 * g_B * g_H;
+                                    CHECK((int64_t)l.grid.x == wide || (int64_t)l.grid.x == narrow);
+                                    CHECK(inside(p.delta, g_B * g_H * g_T * 4));
+                                } else if (is(l, "swa_dkv")) {
+                                    const int64_t sink_wgs = p.pieces * bk, parts = ((int64_t)l.grid.x - sink_wgs) / tiles;
+                                    CHECK(parts * tiles + sink_wgs == (int64_t)l.grid.x && parts == p.splits && parts >= 1);
+                                    // the far queries: behind the window of the first key tile, none lost, no piece empty
+                                    CHECK((p.pieces > 0) == (g_sinks > 0 && g_T > (127 + g_win + 63) / 64 * 64));
+                                    if (p.pieces) CHECK(p.far0 >= 127 + g_win && p.far0 + (int64_t)p.pieces * p.piece_len >= g_T && p.far0 + (int64_t)(p.pieces - 1) * p.piece_len < g_T);
+                                    // written: dk and dv of every key per part, or of the first 64 keys where the far
+                                    // queries' sums are added to them; dk and dv of 64 keys per piece
+                                    const int64_t rows = parts > 1 ? g_T : p.pieces ? (g_T < 64 ? g_T : 64) : 0;
+                                    const int64_t keys = parts * 2 * bk * rows * sums, far = sink_wgs * 2 * 64 * sums;
+                                    CHECK(p.part_rows == rows && inside(p.key_part, keys) && inside(p.sink_part, far));
+                                    CHECK(apart(p.key_part, keys, p.sink_part, far) && apart(p.key_part, keys, p.delta, g_B * g_H * g_T * 4) &&
+                                          apart(p.sink_part, far, p.delta, g_B * g_H * g_T * 4));
+                                    g_parts = rows;
+                                } else {
+                                    CHECK(is(l, "swa_reduce") && g_parts > 0 && (int64_t)l.grid.x == (bk * g_parts * 16 + 255) / 256);
+                                }
+                            };
+                            const long before = g_launches;
+                            CHECK(LIB(gdr2_swa_bwd)(B, T, g_H, Hkv, 64, GDR2_F32, win, sinks, 1.f, A(0), A(1), A(2), nullptr, A(3), F(4), A(5), A(6), A(7), A(8), W(9, n), n, nullptr) == GDR2_OK);
+                            CHECK(g_launches == before + (g_parts ? 3 : 2));
+                        }
+}
+
 int main(int argc, char** argv) {
     g_lib = argc > 1 ? dlopen(argv[1], RTLD_NOW) : nullptr;
     if (!g_lib) {
@@ -233,10 +329,12 @@ int main(int argc, char** argv) {
         return 1;
     }
     norm_fwd();
+    norm_bwd();
     glr();
     decode();
     fill();
     attention();
+    attention_parts();
     if (g_fail) return 1;
     std::printf("ok %ld launches\n", g_launches);
     return 0;
