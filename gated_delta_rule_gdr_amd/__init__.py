@@ -591,6 +591,18 @@ def _need_tensor(name, t, ndim=None):
         raise ValueError(f"{name} must be a {ndim}-D tensor")
 
 
+def _whole(name, x):
+    """x as an argument of 64 bits: ctypes would cut a larger number, int() a fraction."""
+    if type(x) is not int:
+        n = int(x)
+        if n != x:
+            raise ValueError(f"{name} must be a whole number; got {x!r}")
+        x = n
+    if not -(1 << 63) <= x < 1 << 63:
+        raise ValueError(f"{name} does not fit 64 bits: {x}")
+    return x
+
+
 def layer_norm_bwd_workspace_bytes(rows, D):
     return load_library().gdr2_layer_norm_bwd_workspace_bytes(rows, D)
 
@@ -604,11 +616,11 @@ def glr_bwd_workspace_bytes(B, T, D):
 
 
 def swa_bwd_workspace_bytes(B, T, H, Hkv, d, window, sinks=0):
-    return load_library().gdr2_swa_bwd_workspace_bytes(B, T, H, Hkv, d, window, sinks)
+    return load_library().gdr2_swa_bwd_workspace_bytes(B, T, H, Hkv, d, _whole("window", window), _whole("sinks", sinks))
 
 
 def swa_decode_workspace_bytes(N, H, Hkv, d, window, sinks=0):
-    return load_library().gdr2_swa_decode_workspace_bytes(N, H, Hkv, d, window, sinks)
+    return load_library().gdr2_swa_decode_workspace_bytes(N, H, Hkv, d, _whole("window", window), _whole("sinks", sinks))
 
 
 def _norm_inputs(x, weight):
@@ -746,10 +758,11 @@ def gdr2_swa_fwd(q, k, v, window, sinks=0, scale=None, lengths=None):
     dev = _swa_inputs(q, k, v, 4)
     B, T, H, d = q.shape
     _need("lengths", lengths, (B,), torch.int32, dev, optional=True)
+    window, sinks = _whole("window", window), _whole("sinks", sinks)
     _on_gpu(dev)
     o = torch.empty_like(q)
     lse = torch.empty((B, H, T), dtype=torch.float32, device=dev)
-    _run("gdr2_swa_fwd", dev, lib.gdr2_swa_fwd, B, T, H, k.shape[2], d, _dtype(q), int(window), int(sinks),
+    _run("gdr2_swa_fwd", dev, lib.gdr2_swa_fwd, B, T, H, k.shape[2], d, _dtype(q), window, sinks,
          _swa_scale(scale, d), _ptr(q), _ptr(k), _ptr(v), _ptr(lengths), _ptr(o), _ptr(lse))
     return o, lse
 
@@ -766,8 +779,8 @@ def gdr2_swa_bwd(q, k, v, o, lse, dO, window, sinks=0, scale=None, lengths=None,
     _need("lengths", lengths, (B,), torch.int32, dev, optional=True)
     if workspace is not None:
         _ws("workspace", workspace, dev)
+    window, sinks = _whole("window", window), _whole("sinks", sinks)
     _on_gpu(dev)
-    window, sinks = int(window), int(sinks)
     g = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v))
     ws = _new_ws(workspace, lib.gdr2_swa_bwd_workspace_bytes(B, T, H, k.shape[2], d, window, sinks), dev)
     _run("gdr2_swa_bwd", dev, lib.gdr2_swa_bwd, B, T, H, k.shape[2], d, _dtype(q), window, sinks,
@@ -793,9 +806,10 @@ def gdr2_swa_cache_fill(k, v, k_cache, v_cache, sinks=0, lengths=None):
     dev = _swa_inputs(k, k, v, 4)
     B, T, Hkv, d = k.shape
     _need("lengths", lengths, (B,), torch.int32, dev, optional=True)
-    window = _swa_cache(k, k_cache, v_cache, int(sinks), dev)
+    sinks = _whole("sinks", sinks)
+    window = _swa_cache(k, k_cache, v_cache, sinks, dev)
     _on_gpu(dev)
-    _run("gdr2_swa_cache_fill", dev, lib.gdr2_swa_cache_fill, B, T, Hkv, d, _dtype(k), window, int(sinks), _ptr(k),
+    _run("gdr2_swa_cache_fill", dev, lib.gdr2_swa_cache_fill, B, T, Hkv, d, _dtype(k), window, sinks, _ptr(k),
          _ptr(v), _ptr(lengths), _ptr(k_cache), _ptr(v_cache))
 
 
@@ -806,7 +820,7 @@ def gdr2_swa_decode_step(q, k, v, k_cache, v_cache, pos, sinks=0, scale=None, wo
     lib = load_library()
     dev = _swa_inputs(q, k, v, 3)
     N, H, d = q.shape
-    sinks = int(sinks)
+    sinks = _whole("sinks", sinks)
     _need("pos", pos, (N,), torch.int32, dev)
     window = _swa_cache(k, k_cache, v_cache, sinks, dev)
     if workspace is not None:
