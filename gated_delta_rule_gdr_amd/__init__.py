@@ -746,7 +746,7 @@ def _swa_inputs(q, k, v, ndim):
 
 
 def _swa_scale(scale, d):
-    return float(d) ** -0.5 if scale is None else float(scale)
+    return float(d or 1) ** -0.5 if scale is None else float(scale)   # (the library refuses d = 0)
 
 
 def gdr2_swa_fwd(q, k, v, window, sinks=0, scale=None, lengths=None):

@@ -43,3 +43,7 @@ def test_whole_numbers_of_other_types_stay_accepted():
     q, k, v = _attention()
     with pytest.raises(ValueError, match="GPU tensors"):
         g2.gdr2_swa_fwd(q, k, v, 3.0, sinks=torch.tensor(1))
+
+
+def test_empty_heads_have_a_scale():
+    assert g2._swa_scale(None, 64) == 0.125 and g2._swa_scale(0.3, 0) == 0.3 and g2._swa_scale(None, 0) == 1.0
