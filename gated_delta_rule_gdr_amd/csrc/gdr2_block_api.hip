@@ -137,7 +137,7 @@ gdr2_status gdr2_layer_norm_fwd(int64_t rows, int64_t D, gdr2_dtype dt, const vo
     if (!(eps > 0.f) || !(eps < 1e30f)) return GDR2_E_VALUE;
     if (rows == 0) return GDR2_OK;
     if (!x || !weight || !y) return GDR2_E_NULL;
-    if (!all_aligned({x, weight, bias, y, mean, rstd})) return GDR2_E_ALIGN;
+    if (!all_aligned({x, weight, bias, y}) || !aligned4(mean) || !aligned4(rstd)) return GDR2_E_ALIGN;
     const size_t n = (size_t)rows * D * esize(dt), w = (size_t)D * 4, r = (size_t)rows * 4;
     const Range ins[] = {{x, n}, {weight, w}, {bias, w}}, outs[] = {{y, n}, {mean, r}, {rstd, r}};
     if (any_alias(outs, 3, ins, 3)) return GDR2_E_ALIAS;
@@ -161,7 +161,7 @@ gdr2_status gdr2_layer_norm_bwd(int64_t rows, int64_t D, gdr2_dtype dt, const vo
     if (st != GDR2_OK) return st;
     if (!dweight) return GDR2_E_NULL;
     if (rows > 0 && (!x || !weight || !mean || !rstd || !dy || !dx)) return GDR2_E_NULL;
-    if (!all_aligned({x, weight, mean, rstd, dy, dx, dweight, dbias, workspace})) return GDR2_E_ALIGN;
+    if (!all_aligned({x, weight, dy, dx, dweight, dbias, workspace}) || !aligned4(mean) || !aligned4(rstd)) return GDR2_E_ALIGN;
     const size_t need = gdr2_layer_norm_bwd_workspace_bytes(rows, D);
     if (rows > 0 && (!workspace || workspace_bytes < need)) return GDR2_E_WORKSPACE;
     const size_t n = (size_t)rows * D * esize(dt), w = (size_t)D * 4, r = (size_t)rows * 4;
@@ -262,7 +262,7 @@ gdr2_status gdr2_swa_fwd(int64_t B, int64_t T, int64_t H, int64_t Hkv, int64_t d
     if (!scale_ok(scale)) return GDR2_E_VALUE;
     if (B == 0 || T == 0 || H == 0) return GDR2_OK;
     if (!q || !k || !v || !o || !lse) return GDR2_E_NULL;
-    if (!all_aligned({q, k, v, o, lse}) || !aligned4(lengths)) return GDR2_E_ALIGN;
+    if (!all_aligned({q, k, v, o}) || !aligned4(lse) || !aligned4(lengths)) return GDR2_E_ALIGN;
     const size_t nq = (size_t)B * T * H * d * esize(dt), nk = (size_t)B * T * Hkv * d * esize(dt);
     const Range ins[] = {{q, nq}, {k, nk}, {v, nk}, {lengths, (size_t)B * 4}};
     const Range outs[] = {{o, nq}, {lse, (size_t)B * T * H * 4}};
@@ -289,7 +289,7 @@ gdr2_status gdr2_swa_bwd(int64_t B, int64_t T, int64_t H, int64_t Hkv, int64_t d
     if (!scale_ok(scale)) return GDR2_E_VALUE;
     if (B == 0 || T == 0 || H == 0) return GDR2_OK;
     if (!q || !k || !v || !o || !lse || !dO || !dq || !dk || !dv) return GDR2_E_NULL;
-    if (!all_aligned({q, k, v, o, lse, dO, dq, dk, dv, workspace}) || !aligned4(lengths)) return GDR2_E_ALIGN;
+    if (!all_aligned({q, k, v, o, dO, dq, dk, dv, workspace}) || !aligned4(lse) || !aligned4(lengths)) return GDR2_E_ALIGN;
     const SwaBwdWs w = swa_bwd_layout(B, T, H, Hkv, d, window, sinks);
     if (!workspace || workspace_bytes < w.total) return GDR2_E_WORKSPACE;
     const size_t nq = (size_t)B * T * H * d * esize(dt), nk = (size_t)B * T * Hkv * d * esize(dt);

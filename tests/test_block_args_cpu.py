@@ -47,3 +47,18 @@ def test_whole_numbers_of_other_types_stay_accepted():
 
 def test_empty_heads_have_a_scale():
     assert g2._swa_scale(None, 64) == 0.125 and g2._swa_scale(0.3, 0) == 0.3 and g2._swa_scale(None, 0) == 1.0
+
+
+def test_statistics_need_four_byte_alignment():
+    """mean, rstd and lse are read and written as single numbers.  Refused calls only: a later check's status
+    shows that the alignment passed."""
+    lib = g2.load_library()
+    at = lambda i: 0x100000 * (i + 1)  # noqa: E731
+    E_ALIGN, E_ALIAS, E_WS = 5, 6, 7
+    for off, alias, ws in ((4, E_ALIAS, E_WS), (2, E_ALIGN, E_ALIGN)):
+        for m, r in ((at(3) + off, at(4)), (at(3), at(4) + off)):
+            assert lib.gdr2_layer_norm_fwd(4, 64, 1, at(0), at(1), None, 1e-5, at(0), m, r, None) == alias
+            assert lib.gdr2_layer_norm_bwd(4, 64, 1, at(0), at(1), m, r, at(5), at(6), at(7), None, at(8), 0, None) == ws
+        q = (1, 8, 2, 1, 64, 1, 4, 0, 0.1, at(0), at(1), at(2), None)
+        assert lib.gdr2_swa_fwd(*q, at(0), at(4) + off, None) == alias
+        assert lib.gdr2_swa_bwd(*q, at(3), at(4) + off, at(5), at(6), at(7), at(8), at(9), 0, None) == ws

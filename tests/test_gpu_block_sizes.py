@@ -124,3 +124,22 @@ def test_recurrence_rounds_once_per_group():
     # R_t h_{t-1}: the state rebuilt from the one that enters the segment of 128
     P = G * (H - c)
     assert ((g["dlog_a"][0].double() - P).abs() <= (nf + nb + 16) * step * P).all()
+
+
+def test_statistics_at_four_byte_offsets():
+    """mean, rstd and lse as slices of a larger buffer: an odd number of rows puts the second one off 16 bytes."""
+    gen = torch.Generator().manual_seed(62)
+    x, dy = (torch.randn(2, 13, 72, generator=gen).to(DEV) for _ in range(2))
+    w = torch.randn(72, generator=gen).to(DEV)
+    y, mean, rstd = g2.gdr2_layer_norm_fwd(x, w)
+    q, k, v, dO = (torch.randn(1, 13, h, 64, generator=gen).to(DEV) for h in (3, 1, 1, 3))
+    o, lse = g2.gdr2_swa_fwd(q, k, v, 5)
+    buf = torch.zeros(26 + 26 + 39 + 1, device=DEV)
+    m, r, s = buf[1:27].view(2, 13), buf[27:53].view(2, 13), buf[53:].view(1, 3, 13)
+    for dst, src in ((m, mean), (r, rstd), (s, lse)):
+        dst.copy_(src)
+        assert dst.data_ptr() % 16
+    a, b = g2.gdr2_layer_norm_bwd(x, w, m, r, dy), g2.gdr2_layer_norm_bwd(x, w, mean, rstd, dy)
+    assert all(torch.equal(a[n], b[n]) for n in a)
+    a, b = g2.gdr2_swa_bwd(q, k, v, o, s, dO, 5), g2.gdr2_swa_bwd(q, k, v, o, lse, dO, 5)
+    assert all(torch.equal(a[n], b[n]) for n in a)
