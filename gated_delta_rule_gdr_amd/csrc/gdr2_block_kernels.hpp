@@ -95,7 +95,8 @@ struct SwaCut {
 };
 // Workgroups of 128 keys fill the card once there are as many as compute units (256); with fewer, the
 // queries of a tile are cut into up to eight parts of at least two tiles of 64, towards the workgroups the
-// card holds: d=64 bf16 two per unit, d=128 one, unless whole parts leave an eighth of the units idle.
+// card holds: d=64 bf16 two per unit, d=128 one, unless whole parts leave an eighth of the units idle.  (The type
+// is not asked: the workspace query does not know it.  fp32 d=64 holds one per unit and is cut for two.)
 // Backward in us uncut / up to four / eight / sixteen parts: T=2048 H=16/4 d=128 window 2048 bf16 356 / 155 / 152 /
 // 182, T=512 H=8/2 d=64 70 / 34 / 28 / 29, B=2 T=777 H=6/2 d=64 fp32 202 / 88 / 75 / 76; cut at 256 workgroups
 // too: T=4096 H=8 d=128 162 -> 195.  Towards one / two per unit, T=4096 window 2048 d=128: 4 heads (128
@@ -147,7 +148,7 @@ struct SwaDecodeParams {
     const int* pos;         // [N] position of the new token; negative: no token
     void* o;                // [N][H][d]
     int splits;             // parts of the slots per (sequence, key/value head, head group)
-    float* part;            // splits > 1: [N][Hkv][groups][splits][16][d + 2] fp32
+    float* part;            // splits > 1: [N][Hkv][groups][splits][16][d + 4] fp32 (a row, its maximum and sum)
 };
 int swa_decode_splits(long N, long Hkv, long groups, long slots);
 hipError_t swa_decode_dispatch(int dtype_bf16, const SwaDecodeParams& p, hipStream_t s);

@@ -16,8 +16,9 @@
 // not fill the card, the queries of a tile are cut into parts too.  gdr2_swa_reduce_kernel adds such
 // sums in a fixed order.
 //
-// Bound by the matrix products' issue, and the second kernel also by its registers (dk, dv, k and v of 32
-// keys leave one wave per SIMD).  B=4 T=4096 H=16 d=128 window 2048 bf16: dq 339 us (914 TFLOP/s over its
+// No pipe is full: at the size below the matrix units are busy 43 % (dq) and 28 % (dkv) of the cycles, the LDS pipe
+// 30 and 22 %.  The bound is the chain of a tile, probabilities to score gradients to products, over two waves per
+// SIMD (dq, 247 registers) and one (dkv: dk, dv, k and v of 32 keys and the staged tiles take 416).  B=4 T=4096 H=16 d=128 window 2048 bf16: dq 339 us (914 TFLOP/s over its
 // three products), dkv 596 us (693 over its four), reduction 5 us.  Measured there and not kept, for the
 // whole backward (953-956 us): dv and dk on different waves, each forming the probabilities, 981; the
 // same with the probabilities handed over through LDS 948, but 87 us instead of 69 at B=3 T=1537 H=12/3
@@ -29,7 +30,9 @@ namespace gdr2 {
 // Key tiles (of 64) up to which delta is summed from the probabilities.  Normwise error of dq against fp64
 // (d=128 bf16, no window), delta from o / summed: T=16 3.0e-3 / 2.6e-3, T=64 2.7e-3 / 2.5e-3, T=256 2.55e-3 /
 // 2.43e-3, T=1024 2.50e-3 / 2.41e-3; the walk costs 38 -> 43 us of the backward at B=1 T=256 H=64, and
-// 954 -> 1193 us at B=4 T=4096 H=16 window 2048 if every query walked (with four tiles: no change).
+// 954 -> 1193 us at B=4 T=4096 H=16 window 2048 if every query walked (with four tiles: no change).  Windows of up to
+// 129 tokens (193 with 64 queries per workgroup) and no sinks keep every query of any sequence at four tiles, so they
+// always pay it: B=4 T=4096 H=16 window 64 / 128, backward 240 / 262 -> 265 / 298 us, dq's error 2.42e-3 -> 2.36e-3.
 constexpr int kExactTiles = 4;
 
 // KS = 2: 64 queries per workgroup, its halves walk alternate 32-key blocks (as in the forward).

@@ -10,10 +10,12 @@
 // gives few workgroups for the card (kSwaNarrowMost), it takes 64 queries and its two halves (KS = 2)
 // walk alternate 32-key blocks, joined at the end.
 //
-// Bound by the matrix products' issue: two waves per SIMD, one's exponentials beside the other's products.
+// No pipe is full: the matrix units are busy 37 % of the cycles at the first size below and 43 % at the second, the
+// LDS pipe 29 and 34 %.  The bound is the chain of a tile, scores to exponentials to products, which two waves per SIMD
+// (241 registers, 32 of them for tiles on their way to LDS) overlap only in part.
 // B=4 T=4096 H=16 d=128 window 2048 bf16: 251 us, 823 TFLOP/s over the visible pairs (a library product of
 // 8192^3 random bf16 reaches 1275 on the same card); T=32768, four heads to a key head: 610 us, 874 TFLOP/s.
-// With the work between the products taken out it still needs 193 us.  Measured at the first size and
+// With the work between the products taken out, the products and their operands' reads in order still need 193 us.  Measured at the first size and
 // not kept, against 257 us in the same runs: scores formed one tile ahead of their softmax in the same wave 313 us; 64 queries per wave
 // (one wave per SIMD) 469; two wave groups alternating products and softmax behind barriers 286; three
 // waves per SIMD with 32-key tiles 259.
