@@ -100,8 +100,9 @@ struct Swa {
         return c;
     }
     // acc[db][d][n] += sum over the rows r0 + crow(r, h) of tile[row][32 db + d] w[r] (for bf16 the
-    // weights are rounded to bf16: the products' inputs, relative error 2^-8 each, summed in fp32)
-    template <int M>
+    // weights are rounded to bf16: the products' inputs, relative error 2^-8 each, summed in fp32; FINE adds the
+    // product of what that rounding left, 2^-16 each)
+    template <int M, bool FINE = false>
     static __device__ __forceinline__ void add_rows(f32x16 (&acc)[DB], const i32x4* t, int r0, const f32x16& w) {
         const int l = lane_id(), h = l >> 5;
         if constexpr (ES == 2) {
@@ -111,6 +112,11 @@ struct Swa {
                 bf16x8 b;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) b[e] = (bf16)w[8 * kk + e];
+                bf16x8 rest;
+                if constexpr (FINE) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) rest[e] = (bf16)(w[8 * kk + e] - (float)b[e]);
+                }
                 const int ra = r0 + 16 * kk + 4 * h + (p >> 2), rb = ra + 8;
 #pragma unroll
                 for (int db = 0; db < DB; ++db) {
@@ -119,6 +125,7 @@ struct Swa {
                     const bf16x4 hi = ds_read_tr4((const bf16*)(t + at<M>(rb, db, c)) + 4 * (p & 1));
                     const bf16x8 a = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
                     acc[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc[db], 0, 0, 0);
+                    if constexpr (FINE) acc[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, rest, acc[db], 0, 0, 0);
                 }
             }
         } else {

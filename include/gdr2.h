@@ -457,7 +457,8 @@ gdr2_status gdr2_glr_step(int64_t N, int64_t D, gdr2_dtype dtype, const void* x,
  * With GDR2_BF16 the probabilities (forward, backward and decode) and the score gradients are each rounded to bf16
  * once, as inputs of the matrix products, while the softmax' denominator sums them unrounded; and the backward
  * takes sum_c dO_c o_c of a row from the bf16 o, except in rows of few keys.  The normwise error against exact
- * arithmetic on the same inputs is about 1.4 times that of one rounding of the results.
+ * arithmetic on the same inputs is about 1.4 times that of one rounding of the results.  For T <= 32, where the sums
+ * are too short for such roundings to average out, the backward's product inputs keep 16 bits.
  */
 gdr2_status gdr2_swa_fwd(int64_t B, int64_t T, int64_t H, int64_t Hkv, int64_t d, gdr2_dtype dtype,
                          int64_t window, int64_t sinks, float scale, const void* q, const void* k,
