@@ -17,7 +17,7 @@
 // sums in a fixed order.
 //
 // No pipe is full: at the size below the matrix units are busy 43 % (dq) and 28 % (dkv) of the cycles, the LDS pipe
-// 30 and 22 %.  The bound is the chain of a tile, probabilities to score gradients to products, over two waves per
+// 29 and 22 %.  The bound is the chain of a tile, probabilities to score gradients to products, over two waves per
 // SIMD (dq, 247 registers) and one (dkv: dk, dv, k and v of 32 keys and the staged tiles take 416).  B=4 T=4096 H=16 d=128 window 2048 bf16: dq 339 us (914 TFLOP/s over its
 // three products), dkv 596 us (693 over its four), reduction 5 us.  Measured there and not kept, for the
 // whole backward (953-956 us): dv and dk on different waves, each forming the probabilities, 981; the

@@ -11,7 +11,7 @@
 // walk alternate 32-key blocks, joined at the end.
 //
 // No pipe is full: the matrix units are busy 37 % of the cycles at the first size below and 43 % at the second, the
-// LDS pipe 29 and 34 %.  The bound is the chain of a tile, scores to exponentials to products, which two waves per SIMD
+// LDS pipe 29 and 33 %.  The bound is the chain of a tile, scores to exponentials to products, which two waves per SIMD
 // (241 registers, 32 of them for tiles on their way to LDS) overlap only in part.
 // B=4 T=4096 H=16 d=128 window 2048 bf16: 251 us, 823 TFLOP/s over the visible pairs (a library product of
 // 8192^3 random bf16 reaches 1275 on the same card); T=32768, four heads to a key head: 610 us, 874 TFLOP/s.
