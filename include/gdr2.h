@@ -380,10 +380,10 @@ gdr2_status gdr2_out_gate_bwd(int64_t rows, int64_t dv, gdr2_dtype dtype, const 
  * attention beside the recurrent mixer (ainews.random.gg article on Gated DeltaNet-2, section "Block
  * design and hybrid model": a 2K attention window), and an elementwise gated recurrence.  The
  * conventions at the top of this header hold; x, q, k, v, o, y, h, their gradients and the caches
- * have the caller's dtype, everything else is fp32.  mean, rstd, lse and the int32 arrays (lengths, positions)
- * need 4-byte alignment only.  int32 arrays live in device memory; their values are not visible to the host checks, so every value has a
- * meaning (below).  Rows at and behind a sequence's length, and cache slots not written yet, may hold
- * anything.  A NaN or infinity stays in its row (layer norm; its weight gradients excepted), its
+ * have the caller's dtype, everything else is fp32.  mean, rstd, lse and the int32 arrays (lengths,
+ * positions) need 4-byte alignment only.  The int32 arrays live in device memory; their values are not
+ * visible to the host checks, so every value has a meaning (below).  Rows at and behind a sequence's
+ * length, and cache slots not written yet, may hold anything.  A NaN or infinity stays in its row (layer norm; its weight gradients excepted), its
  * channel (recurrence) or its sequence and key/value head (attention, whose products are formed over
  * tiles: there it may also reach rows of that sequence that do not see it).  A workspace serves one
  * call at a time: calls, or captured graphs, that may run at the same time need their own (with a shared one
