@@ -18,6 +18,12 @@ Around the mixer, in a hybrid stack:
   gdr2_swa_cache_fill(k, v, k_cache, v_cache, sinks) / gdr2_swa_decode_step(q, k, v, k_cache, v_cache, pos, sinks)
   gdr2_glr_fwd(x, log_a, h0) -> (h, h_T, fwd_ws) / gdr2_glr_bwd(x, log_a, dh, fwd_ws, dh_T)
   gdr2_glr_step(x, log_a, h_in, h_out)
+  gdr2_rms_norm_fwd(x, weight, residual) -> (y, h, rstd) / gdr2_rms_norm_bwd(h, weight, rstd, dy, dh)
+  gdr2_rms_norm_q8_fwd(x, weight, residual, group=0) -> (y8, scale, h)
+  gdr2_dla_fwd(q, k, v, log_decay, S0, lengths) -> (o, S_T) / gdr2_dla_bwd(q, k, v, log_decay, dO, S0, dS_T, lengths)
+  gdr2_dla_step(q, k, v, log_decay, S_in, S_out) -> (o, S_out)
+  gdr2_paged_cache_fill(k, v, k_pages, v_pages, page_table, start, lengths)
+  gdr2_paged_decode_step(q, k, v, k_pages, v_pages, page_table, pos) -> o
 Each of b, w and log_alpha may be channel-wise ([..., d]) or a scalar per head (the token shape of
 q without its channel axis); the gate-shape bits passed to the *_ex entry points follow from the
 shapes, and the gradients come back in the shape of their gate.  ``prologue=Prologue(c, eps)``
@@ -43,7 +49,10 @@ __all__ = ["gdr2_fwd_chunked", "gdr2_bwd_chunked", "gdr2_decode_step", "gdr2_fwd
            "gdr2_glr_step", "gdr2_swa_fwd", "gdr2_swa_bwd", "gdr2_swa_cache_fill",
            "gdr2_swa_decode_step", "glr_fwd_workspace_bytes", "glr_bwd_workspace_bytes",
            "layer_norm_bwd_workspace_bytes", "swa_bwd_workspace_bytes",
-           "swa_decode_workspace_bytes"]
+           "swa_decode_workspace_bytes", "gdr2_rms_norm_fwd", "gdr2_rms_norm_bwd", "gdr2_rms_norm_q8_fwd",
+           "rms_norm_bwd_workspace_bytes", "gdr2_dla_fwd", "gdr2_dla_bwd", "gdr2_dla_step",
+           "dla_fwd_workspace_bytes", "dla_bwd_workspace_bytes", "gdr2_paged_cache_fill",
+           "gdr2_paged_decode_step", "paged_decode_workspace_bytes"]
 
 CHUNK = 64
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -156,13 +165,24 @@ def load_library():
             ("gdr2_swa_fwd", [I64] * 5 + [I, I64, I64, F] + [P] * 7),
             ("gdr2_swa_bwd", [I64] * 5 + [I, I64, I64, F] + [P] * 11 + [SZ, P]),
             ("gdr2_swa_cache_fill", [I64] * 4 + [I, I64, I64] + [P] * 6),
-            ("gdr2_swa_decode_step", [I64] * 4 + [I, I64, I64, F] + [P] * 8 + [SZ, P])):
+            ("gdr2_swa_decode_step", [I64] * 4 + [I, I64, I64, F] + [P] * 8 + [SZ, P]),
+            ("gdr2_rms_norm_fwd", [I64, I64, I, P, P, P, F] + [P] * 4),
+            ("gdr2_rms_norm_q8_fwd", [I64, I64, I, I64, P, P, P, F] + [P] * 4),
+            ("gdr2_rms_norm_bwd", [I64, I64, I] + [P] * 8 + [SZ, P]),
+            ("gdr2_dla_fwd", [I64] * 5 + [I] + [P] * 9 + [SZ, P]),
+            ("gdr2_dla_bwd", [I64] * 5 + [I] + [P] * 13 + [SZ, P]),
+            ("gdr2_dla_step", [I64] * 4 + [I] + [P] * 8),
+            ("gdr2_paged_cache_fill", [I64] * 4 + [I] + [I64] * 3 + [P] * 8),
+            ("gdr2_paged_decode_step", [I64] * 4 + [I] + [I64] * 3 + [F] + [P] * 9 + [SZ, P])):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = I
     for name, n in (("gdr2_layer_norm_bwd", 2), ("gdr2_glr_fwd", 3), ("gdr2_glr_bwd", 3),
-                    ("gdr2_swa_bwd", 7), ("gdr2_swa_decode", 6)):
+                    ("gdr2_swa_bwd", 7), ("gdr2_swa_decode", 6), ("gdr2_rms_norm_bwd", 2), ("gdr2_paged_decode", 6)):
         getattr(lib, name + "_workspace_bytes").argtypes = [I64] * n
         getattr(lib, name + "_workspace_bytes").restype = SZ
+    for name in ("gdr2_dla_fwd_workspace_bytes", "gdr2_dla_bwd_workspace_bytes"):
+        getattr(lib, name).argtypes = [I64] * 5 + [I]
+        getattr(lib, name).restype = SZ
     lib.gdr2_fwd_workspace_bytes.argtypes = [I64] * 5 + [ctypes.c_int]
     lib.gdr2_fwd_workspace_bytes.restype = SZ
     lib.gdr2_bwd_workspace_bytes.argtypes = [I64] * 5 + [ctypes.c_int]
@@ -834,4 +854,215 @@ def gdr2_swa_decode_step(q, k, v, k_cache, v_cache, pos, sinks=0, scale=None, wo
     _run("gdr2_swa_decode_step", dev, lib.gdr2_swa_decode_step, N, H, k.shape[1], d, _dtype(q), window, sinks,
          _swa_scale(scale, d), _ptr(q), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(pos), _ptr(o), _ptr(ws),
          ws.numel() if ws is not None else 0)
+    return o
+
+
+# ---------------------------------------------------------------------------------------------
+# The residual stream's norm, linear attention with a decay per head, the paged cache.
+def _maybe_ws(workspace, need, dev):
+    """The caller's workspace, a new one, or none where none is needed."""
+    if workspace is not None or not need:
+        return workspace
+    return torch.empty(need, dtype=torch.uint8, device=dev)
+
+
+def _ws_args(ws):
+    return _ptr(ws), ws.numel() if ws is not None else 0
+
+
+def rms_norm_bwd_workspace_bytes(rows, D):
+    return load_library().gdr2_rms_norm_bwd_workspace_bytes(rows, D)
+
+
+def dla_fwd_workspace_bytes(B, T, H, dk, dv, dtype):
+    return load_library().gdr2_dla_fwd_workspace_bytes(B, T, H, dk, dv, _dt_code(dtype))
+
+
+def dla_bwd_workspace_bytes(B, T, H, dk, dv, dtype):
+    return load_library().gdr2_dla_bwd_workspace_bytes(B, T, H, dk, dv, _dt_code(dtype))
+
+
+def paged_decode_workspace_bytes(N, H, Hkv, d, page, width):
+    return load_library().gdr2_paged_decode_workspace_bytes(N, H, Hkv, d, page, width)
+
+
+def _rms_inputs(x, weight, residual, h_out):
+    """Checks, and the stream h: x itself without a residual, else h_out or a new buffer."""
+    dev, rows, D = _norm_inputs(x, weight)
+    _need("residual", residual, x.shape, x.dtype, dev, optional=True)
+    _need("h_out", h_out, x.shape, x.dtype, dev, optional=True)
+    if h_out is not None and residual is None:
+        raise ValueError("h_out needs a residual: without one the stream is x")
+    _on_gpu(dev)
+    h = x if residual is None else h_out if h_out is not None else torch.empty_like(x)
+    return dev, rows, D, h
+
+
+def gdr2_rms_norm_fwd(x, weight, residual=None, eps=1e-6, h_out=None):
+    """RMS norm over the last axis of the stream h = x + residual (kept in x's dtype, and normalised as
+    kept; x itself without a residual): x and residual [..., D] (D a multiple of 8, up to 16384), weight [D]
+    fp32.  ``h_out`` may be ``residual`` itself (the stream in place).  Returns (y, h, rstd), rstd [...] fp32
+    for the backward."""
+    lib = load_library()
+    dev, rows, D, h = _rms_inputs(x, weight, residual, h_out)
+    y = torch.empty_like(x)
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    _run("gdr2_rms_norm_fwd", dev, lib.gdr2_rms_norm_fwd, rows, D, _dtype(x), _ptr(x), _ptr(residual), _ptr(weight),
+         float(eps), None if residual is None else _ptr(h), _ptr(y), _ptr(rstd))
+    return y, h, rstd
+
+
+def gdr2_rms_norm_q8_fwd(x, weight, residual=None, eps=1e-6, group=0, h_out=None):
+    """The same norm with an 8-bit result: y8 [..., D] torch.float8_e4m3fn and fp32 scales with y about
+    y8 * scale, one per row (group 0: scale [...]) or per group of 32, 64 or 128 channels (scale
+    [..., ceil(D / group)]).  Returns (y8, scale, h)."""
+    lib = load_library()
+    group = _whole("group", group)
+    dev, rows, D, h = _rms_inputs(x, weight, residual, h_out)
+    y8 = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=dev)
+    shape = x.shape[:-1] + (-(-D // group),) if group > 0 else x.shape[:-1]
+    scale = torch.empty(shape, dtype=torch.float32, device=dev)
+    _run("gdr2_rms_norm_q8_fwd", dev, lib.gdr2_rms_norm_q8_fwd, rows, D, _dtype(x), group, _ptr(x), _ptr(residual),
+         _ptr(weight), float(eps), None if residual is None else _ptr(h), _ptr(y8), _ptr(scale))
+    return y8, scale, h
+
+
+def gdr2_rms_norm_bwd(h, weight, rstd, dy, dh=None, workspace=None):
+    """Backward of gdr2_rms_norm_fwd for the cotangents dy of y and dh of the stream h (None = zero), with
+    the forward's h and rstd.  Returns dict dx (the gradient of x and of residual alike), dweight."""
+    lib = load_library()
+    dev, rows, D = _norm_inputs(h, weight)
+    _need("rstd", rstd, h.shape[:-1], torch.float32, dev)
+    _need("dy", dy, h.shape, h.dtype, dev)
+    _need("dh", dh, h.shape, h.dtype, dev, optional=True)
+    if workspace is not None:
+        _ws("workspace", workspace, dev)
+    _on_gpu(dev)
+    ws = _new_ws(workspace, lib.gdr2_rms_norm_bwd_workspace_bytes(rows, D), dev)
+    g = dict(dx=torch.empty_like(h), dweight=torch.empty_like(weight))
+    _run("gdr2_rms_norm_bwd", dev, lib.gdr2_rms_norm_bwd, rows, D, _dtype(h), _ptr(h), _ptr(weight), _ptr(rstd), _ptr(dy),
+         _ptr(dh), _ptr(g["dx"]), _ptr(g["dweight"]), _ptr(ws), ws.numel())
+    return g
+
+
+def _dla_inputs(q, k, v, log_decay, ndim):
+    _need_tensor("q", q, ndim)
+    _need_tensor("v", v, ndim)
+    _dtype(q)
+    dev = q.device
+    _need("q", q, q.shape, q.dtype, dev)
+    _need("k", k, q.shape, q.dtype, dev)
+    _need("v", v, q.shape[:-1] + v.shape[-1:], q.dtype, dev)
+    _need("log_decay", log_decay, (q.shape[-2],), torch.float32, dev)
+    return dev, (q.shape[0],) + q.shape[-2:] + v.shape[-1:]      # the states' shape
+
+
+def gdr2_dla_fwd(q, k, v, log_decay, S0=None, lengths=None, want_final_state=True, workspace=None):
+    """Linear attention with one fixed decay exp(log_decay[h]) per head, S_t = a S_{t-1} + k_t v_t^T,
+    o_t = S_t^T q_t: q, k [B, T, H, dk], v [B, T, H, dv] (dk, dv in {64, 128}; callers scale q), log_decay [H]
+    fp32, S0 [B, H, dk, dv] fp32.  ``lengths`` [B] int32 marks rows at and behind a length as padding (o zero
+    there; S_T is the state at the length).  Returns (o, S_T or None)."""
+    lib = load_library()
+    dev, state = _dla_inputs(q, k, v, log_decay, 4)
+    B, T, H, dk = q.shape
+    _need("S0", S0, state, torch.float32, dev, optional=True)
+    _need("lengths", lengths, (B,), torch.int32, dev, optional=True)
+    if workspace is not None:
+        _ws("workspace", workspace, dev)
+    _on_gpu(dev)
+    dt = _dtype(q)
+    o = torch.empty_like(v)
+    S_T = torch.empty(state, dtype=torch.float32, device=dev) if want_final_state else None
+    ws = _maybe_ws(workspace, lib.gdr2_dla_fwd_workspace_bytes(B, T, H, dk, v.shape[-1], dt), dev)
+    _run("gdr2_dla_fwd", dev, lib.gdr2_dla_fwd, B, T, H, dk, v.shape[-1], dt, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
+         _ptr(S0), _ptr(lengths), _ptr(o), _ptr(S_T), *_ws_args(ws))
+    return o, S_T
+
+
+def gdr2_dla_bwd(q, k, v, log_decay, dO, S0=None, dS_T=None, lengths=None, want_dS0=True, workspace=None):
+    """Backward of gdr2_dla_fwd for the cotangents dO of o and dS_T of S_T (None = zero), with the forward's
+    inputs; it needs nothing else of the forward.  Returns dict dq, dk, dv, dS0 (None if not wanted)."""
+    lib = load_library()
+    dev, state = _dla_inputs(q, k, v, log_decay, 4)
+    B, T, H, dk = q.shape
+    _need("dO", dO, v.shape, q.dtype, dev)
+    _need("S0", S0, state, torch.float32, dev, optional=True)
+    _need("dS_T", dS_T, state, torch.float32, dev, optional=True)
+    _need("lengths", lengths, (B,), torch.int32, dev, optional=True)
+    if workspace is not None:
+        _ws("workspace", workspace, dev)
+    _on_gpu(dev)
+    dt = _dtype(q)
+    g = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
+             dS0=torch.empty(state, dtype=torch.float32, device=dev) if want_dS0 else None)
+    ws = _maybe_ws(workspace, lib.gdr2_dla_bwd_workspace_bytes(B, T, H, dk, v.shape[-1], dt), dev)
+    _run("gdr2_dla_bwd", dev, lib.gdr2_dla_bwd, B, T, H, dk, v.shape[-1], dt, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
+         _ptr(S0), _ptr(lengths), _ptr(dO), _ptr(dS_T), _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dv"]), _ptr(g["dS0"]),
+         *_ws_args(ws))
+    return g
+
+
+def gdr2_dla_step(q, k, v, log_decay, S_in=None, S_out=None):
+    """One token of that attention for N sequences: q, k [N, H, dk], v [N, H, dv], state [N, H, dk, dv] fp32.
+    S_out defaults to S_in (in place) or a new buffer.  Returns (o [N, H, dv], S_out)."""
+    lib = load_library()
+    dev, state = _dla_inputs(q, k, v, log_decay, 3)
+    _need("S_in", S_in, state, torch.float32, dev, optional=True)
+    _need("S_out", S_out, state, torch.float32, dev, optional=True)
+    _on_gpu(dev)
+    if S_out is None:
+        S_out = S_in if S_in is not None else torch.empty(state, dtype=torch.float32, device=dev)
+    o = torch.empty_like(v)
+    N, H, dk = q.shape
+    _run("gdr2_dla_step", dev, lib.gdr2_dla_step, N, H, dk, v.shape[-1], _dtype(q), _ptr(q), _ptr(k), _ptr(v),
+         _ptr(log_decay), _ptr(S_in), _ptr(S_out), _ptr(o))
+    return o, S_out
+
+
+def _paged_inputs(k, k_pages, v_pages, page_table, dev):
+    """Checks the pages [pages, page, Hkv, d] against k [N, ..., Hkv, d] and the table [N, width]; returns
+    (page, pages, width)."""
+    _need_tensor("k_pages", k_pages, 4)
+    shape = k_pages.shape[:2] + k.shape[-2:]
+    _need("k_pages", k_pages, shape, k.dtype, dev)
+    _need("v_pages", v_pages, shape, k.dtype, dev)
+    _need_tensor("page_table", page_table, 2)
+    _need("page_table", page_table, (k.shape[0], page_table.shape[1]), torch.int32, dev)
+    return k_pages.shape[1], k_pages.shape[0], page_table.shape[1]
+
+
+def gdr2_paged_cache_fill(k, v, k_pages, v_pages, page_table, start=None, lengths=None):
+    """Stores a prefill's k and v [B, T, Hkv, d] in a cache of pages (k_pages, v_pages [pages, page, Hkv, d],
+    page a power of two): token t < lengths[b] (T without ``lengths``) of sequence b at position start[b] + t
+    (0 without ``start``), which is row p % page of page page_table[b, p // page].  A position without such a
+    row is left out; other rows keep their contents."""
+    lib = load_library()
+    dev = _swa_inputs(k, k, v, 4)
+    B, T, Hkv, d = k.shape
+    page, pages, width = _paged_inputs(k, k_pages, v_pages, page_table, dev)
+    _need("start", start, (B,), torch.int32, dev, optional=True)
+    _need("lengths", lengths, (B,), torch.int32, dev, optional=True)
+    _on_gpu(dev)
+    _run("gdr2_paged_cache_fill", dev, lib.gdr2_paged_cache_fill, B, T, Hkv, d, _dtype(k), page, pages, width, _ptr(k),
+         _ptr(v), _ptr(start), _ptr(lengths), _ptr(page_table), _ptr(k_pages), _ptr(v_pages))
+
+
+def gdr2_paged_decode_step(q, k, v, k_pages, v_pages, page_table, pos, scale=None, workspace=None):
+    """One token per sequence over everything its pages hold: q [N, H, d], k and v [N, Hkv, d] at position
+    pos [N] int32 (negative: no token, o = 0).  Stores k and v in the pages (in place) and returns o [N, H, d]
+    over the positions 0 .. pos[n]; scale defaults to d^-0.5."""
+    lib = load_library()
+    dev = _swa_inputs(q, k, v, 3)
+    N, H, d = q.shape
+    Hkv = k.shape[1]
+    page, pages, width = _paged_inputs(k, k_pages, v_pages, page_table, dev)
+    _need("pos", pos, (N,), torch.int32, dev)
+    if workspace is not None:
+        _ws("workspace", workspace, dev)
+    _on_gpu(dev)
+    o = torch.empty_like(q)
+    ws = _maybe_ws(workspace, lib.gdr2_paged_decode_workspace_bytes(N, H, Hkv, d, page, width), dev)
+    _run("gdr2_paged_decode_step", dev, lib.gdr2_paged_decode_step, N, H, Hkv, d, _dtype(q), page, pages, width,
+         _swa_scale(scale, d), _ptr(q), _ptr(k), _ptr(v), _ptr(page_table), _ptr(pos), _ptr(k_pages), _ptr(v_pages),
+         _ptr(o), *_ws_args(ws))
     return o

@@ -495,6 +495,121 @@ gdr2_status gdr2_swa_decode_step(int64_t N, int64_t H, int64_t Hkv, int64_t d, g
                                  const int32_t* pos, void* o, void* workspace,
                                  size_t workspace_bytes, void* stream);
 
+/*
+ * ------------------------------------------------------------------------------------------------
+ * More operators of a hybrid stack: the RMS norm of a residual stream, linear attention with a fixed
+ * decay per head in the mixer's place, and a cache of pages for layers that attend to every position.
+ * The conventions of the operators above hold: int32 arrays and rstd need 4-byte alignment, the values
+ * of int32 arrays are not visible to the host checks and every value has a meaning, rows at and behind a
+ * sequence's length may hold anything, and a workspace serves one call at a time.
+ */
+
+/*
+ * RMS norm over rows of D channels (D a multiple of 8, 8 <= D <= 16384, else GDR2_E_UNSUPPORTED;
+ * rows < 2^31) of a stream h = x + residual, which is kept in dtype: what is stored is what is
+ * normalised, so a backward or a recomputation from the stored stream sees the same rows:
+ *     h_j = x_j + residual_j (rounded once),   rstd = 1 / sqrt(sum_j h_j^2 / D + eps),   y_j = h_j rstd weight_j
+ *   x, residual, h, y   [rows][D]  dtype   residual NULL: h_j = x_j, and h must be NULL (else GDR2_E_VALUE);
+ *                                          otherwise h is required and may be residual exactly
+ *   weight              [D]        fp32
+ *   rstd                [rows]     fp32 or NULL (not wanted; the backward reads it)
+ *   eps                 > 0, finite (else GDR2_E_VALUE)
+ * The backward takes the stream h (x without a residual), dy [rows][D] and the stream's own cotangent dh
+ * [rows][D] (NULL = zero) and writes dx [rows][D], which is the gradient of x and of residual alike, and
+ * dweight [D] fp32, added over all rows in a fixed order (zero for rows = 0):
+ *     a_j = dy_j weight_j,  n_j = h_j rstd,  dx_j = dh_j + rstd (a_j - n_j sum_i a_i n_i / D)
+ */
+gdr2_status gdr2_rms_norm_fwd(int64_t rows, int64_t D, gdr2_dtype dtype, const void* x,
+                              const void* residual, const float* weight, float eps, void* h,
+                              void* y, float* rstd, void* stream);
+size_t gdr2_rms_norm_bwd_workspace_bytes(int64_t rows, int64_t D);
+gdr2_status gdr2_rms_norm_bwd(int64_t rows, int64_t D, gdr2_dtype dtype, const void* h,
+                              const float* weight, const float* rstd, const void* dy,
+                              const void* dh, void* dx, float* dweight, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
+ * The same norm with an 8-bit result for the products behind it: y8 holds OCP e4m3 values (1 byte each,
+ * largest 448) of y / scale, rounded once to nearest even from fp32, and scale one fp32 number per row
+ * (group = 0: [rows]) or per group of 32, 64 or 128 channels ([rows][ceil(D / group)]; any other group
+ * GDR2_E_UNSUPPORTED): y_j is about y8_j scale, with
+ *     scale = max |y_j| / 448 over the row or group (0 where every y_j is 0; at least 1e-37 otherwise).
+ * Where a y_j is not finite its scale is NaN and the values under that scale are NaN.  scale needs 4-byte
+ * alignment.  x, residual, weight, eps and h as in gdr2_rms_norm_fwd.
+ */
+gdr2_status gdr2_rms_norm_q8_fwd(int64_t rows, int64_t D, gdr2_dtype dtype, int64_t group,
+                                 const void* x, const void* residual, const float* weight,
+                                 float eps, void* h, void* y8, float* scale, void* stream);
+
+/*
+ * Linear attention with one fixed decay a_h = exp(log_decay_h) per head (no gradient flows to it):
+ *     S_t = a S_{t-1} + k_t v_t^T,   o_t = S_t^T q_t   (the updated state is read, no query scale)
+ * -- the mixer's update without its erase product, computed without the mixer's triangular solve.
+ *   q, k, dq, dk    [B][T][H][dk]  dtype     dk, dv in {64, 128}; T <= 2^30, B H <= 2^20 and
+ *   v, o, dO, dv    [B][T][H][dv]  dtype     B H (ceil(T / 64) + 1) < 2^24 (else GDR2_E_SHAPE)
+ *   log_decay       [H]            fp32      natural log, <= 0 (0: nothing is forgotten; -inf: all of it)
+ *   S0, S_T, dS_T, dS0  [B][H][dk][dv] fp32 or NULL (inputs: zero; outputs: not wanted)
+ *   lengths         [B] int32 or NULL (every sequence has T tokens); clamped to [0, T].  o, dq, dk and dv are
+ *                   zero behind a length, S_T is the state at it, and the gradients are those of that state
+ * The backward takes the inputs alone (it carries the states again):
+ *     R_t = a R_{t+1} + q_t dO_t^T (from dS_T),  dq_t = S_t dO_t,  dk_t = R_t v_t,  dv_t = R_t^T k_t,  dS0 = a R_0
+ * Both need a workspace of the size their query returns (0: none; the sequence is cut where there are few
+ * chains).  gdr2_dla_step is one token for N sequences: S_out = a S_in + k v^T, o = S_out^T q, with S_in
+ * [N][H][dk][dv] fp32 (NULL = zero; may equal S_out exactly); N H < 2^24.
+ * Precision: states and every sum are fp32.  With GDR2_BF16 a decayed operand of the state's sums keeps 16
+ * bits, and scores and the states as read are rounded to bf16 once each, as inputs of the matrix products.
+ * A NaN or infinity stays in its sequence and head (products are formed over tiles: there it may also reach
+ * rows before it).
+ */
+size_t gdr2_dla_fwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t dk, int64_t dv,
+                                    gdr2_dtype dtype);
+gdr2_status gdr2_dla_fwd(int64_t B, int64_t T, int64_t H, int64_t dk, int64_t dv, gdr2_dtype dtype,
+                         const void* q, const void* k, const void* v, const float* log_decay,
+                         const float* S0, const int32_t* lengths, void* o, float* S_T,
+                         void* workspace, size_t workspace_bytes, void* stream);
+size_t gdr2_dla_bwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t dk, int64_t dv,
+                                    gdr2_dtype dtype);
+gdr2_status gdr2_dla_bwd(int64_t B, int64_t T, int64_t H, int64_t dk, int64_t dv, gdr2_dtype dtype,
+                         const void* q, const void* k, const void* v, const float* log_decay,
+                         const float* S0, const int32_t* lengths, const void* dO,
+                         const float* dS_T, void* dq, void* dk_, void* dv_, float* dS0,
+                         void* workspace, size_t workspace_bytes, void* stream);
+gdr2_status gdr2_dla_step(int64_t N, int64_t H, int64_t dk, int64_t dv, gdr2_dtype dtype,
+                          const void* q, const void* k, const void* v, const float* log_decay,
+                          const float* S_in, float* S_out, void* o, void* stream);
+
+/*
+ * A key/value cache of pages: k_pages and v_pages [pages][page][Hkv][d] in dtype, page a power of two,
+ * (else GDR2_E_VALUE), pages * page < 2^31; page_table [N][width] int32, width * page <= 2^30, N * width <= 2^40.  Position p of a sequence n is row
+ * p % page of page page_table[n][p / page].  A position behind the table, or whose entry lies outside of
+ * [0, pages), has no row: nothing is stored at it and attention does not see it.  Sequences may share pages
+ * that no call writes to; rows that one call writes for two tokens hold either token's values.
+ *
+ * gdr2_paged_cache_fill stores, from a prefill's k and v ([B][T][Hkv][d]), token t < lengths[b] of sequence b
+ * at position start[b] + t (lengths NULL: T tokens, values clamped to [0, T]; start NULL: 0; a negative position
+ * has no row).  Other rows are left as they were.
+ * gdr2_paged_decode_step stores the new token's k and v ([N][Hkv][d]) at position pos[n] and returns its
+ * attention output o ([N][H][d]) over the positions 0 .. pos[n]; the new token sees itself whether it has a
+ * row or not.  Query head h reads key/value head h / (H / Hkv).  A negative pos[n] means that sequence has no
+ * token: o is zero, nothing is stored.
+ *   H a multiple of Hkv, H <= 32768, d in {64, 128}, N * H <= 2^30, B * T * Hkv <= 2^32; scale > 0, finite
+ *   workspace   gdr2_paged_decode_workspace_bytes() bytes (0: none needed)
+ * Precision as in gdr2_swa_decode_step: fp32 throughout, but for bf16 probabilities as inputs of their product.
+ */
+gdr2_status gdr2_paged_cache_fill(int64_t B, int64_t T, int64_t Hkv, int64_t d, gdr2_dtype dtype,
+                                  int64_t page, int64_t pages, int64_t width, const void* k,
+                                  const void* v, const int32_t* start, const int32_t* lengths,
+                                  const int32_t* page_table, void* k_pages, void* v_pages,
+                                  void* stream);
+size_t gdr2_paged_decode_workspace_bytes(int64_t N, int64_t H, int64_t Hkv, int64_t d, int64_t page,
+                                         int64_t width);
+gdr2_status gdr2_paged_decode_step(int64_t N, int64_t H, int64_t Hkv, int64_t d, gdr2_dtype dtype,
+                                   int64_t page, int64_t pages, int64_t width, float scale,
+                                   const void* q, const void* k, const void* v,
+                                   const int32_t* page_table, const int32_t* pos, void* k_pages,
+                                   void* v_pages, void* o, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
 /* Static description of a status code. */
 const char* gdr2_status_string(gdr2_status s);
 
