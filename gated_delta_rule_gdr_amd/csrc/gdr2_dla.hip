@@ -8,14 +8,15 @@
 // kept by the forward.  Chunks of 64 tokens: inside a chunk through the scores x_r . y_s, weighted a^(r - s);
 // from before it through the state, out_r += a^(r + 1) x_r S; then S <- a^64 S + sum_s a^(63 - s) y_s z_s^T.
 //
-// A workgroup carries 32 or 64 columns of one chain's state in fp32 registers (columns are independent), over the
+// A workgroup carries 32 columns of one chain's state in fp32 registers (columns are independent), over the
 // whole sequence or, where there are few chains, over one segment of it, whose entering state is put together from
 // the segments' own states (a first launch).  Scores are formed transposed (rows s, columns r), so that a lane's
 // weighted scores are operand values of the next product as they stand; the state is read from a bf16 copy in LDS
-// that each chunk writes for the next one.  Tiles are double buffered in LDS, one barrier per chunk.
+// that each chunk writes for the next one.
 //
 // Rounding: S is carried in fp32, its decay as S + S (a^n - 1), so that slow decays lose nothing over long
-// sequences; the decayed operand of its sums is split into two bf16 (16 bits).  Scores, and S as it is read, are
+// sequences; the decayed operand of its sums is split into bf16 parts: three (24 bits) where the state is a result,
+// two where it is only read, as bf16.  Scores, and S as it is read, are
 // rounded to bf16 once as inputs of their products, whose sums are fp32.  fp32 rounds nothing else.
 #include "gdr2_common.hpp"
 #include "gdr2_hybrid_kernels.hpp"
@@ -23,321 +24,678 @@
 namespace gdr2 {
 
 constexpr int kDlaThreads = 256, C = kDlaChunk;
+constexpr int kDlaVS = 64, kDlaF32VS = 32;  // columns of a workgroup's state
 
 // a^n for whole n >= 0; a^0 = 1 also where a = 0
 __device__ __forceinline__ float dla_pow(float g, int n) { return n == 0 ? 1.f : expf((float)n * g); }
 
-template <typename T, int K, int VS>
-struct Dla {
-    static constexpr int ES = (int)sizeof(T), E16 = 16 / ES;            // elements of a 16-byte piece
-    static constexpr int KP = K * ES / 64;                              // operand pieces of a row per lane
-    static constexpr int PY = K + E16, PZ = VS + E16;                   // LDS pitches, elements
-    static constexpr int YU = C * K * ES / 16 / kDlaThreads, ZU = C * VS * ES / 16 / kDlaThreads;  // pieces a thread stages
-    static constexpr int KB = K / 64, VB = VS / 16;                     // a wave's 16-row blocks of the state, and columns'
-    static_assert(YU >= 1 && ZU >= 1, "staging");
-
-    // products of 16 x 16 by 64 bytes of contraction
-    static __device__ __forceinline__ void mma(f32x4& c, const i32x4& a, const i32x4& b) {
-        if constexpr (ES == 2) {
-            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-        } else {
-            const f32x4 x = __builtin_bit_cast(f32x4, a), y = __builtin_bit_cast(f32x4, b);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x[e], y[e], c, 0, 0, 0);
-        }
+// Tiles in LDS are rows of R 16-byte pieces without padding.  Operands with the contraction along a row are read as one
+// piece of sixteen rows, operands with it down the rows as 64 bytes of four rows; an exclusive or on the piece's number
+// spreads either over all banks.
+template <typename T, int R>
+__device__ __forceinline__ int tile_at(int row, int piece) {
+    if constexpr (sizeof(T) == 2) {
+        const int b = ((row >> 2) ^ (row >> 3)) & 1, t = row >> 1;
+        if constexpr (R == 16) return row * R + (piece ^ ((row & 3) << 2 | b << 1 | ((row >> 2) & 1)));
+        if constexpr (R == 8) return row * R + (piece ^ ((t & 1) << 2 | b << 1 | ((t >> 1) & 1)));
+        return row * R + piece;  // four rows of 64 bytes are all banks
+    } else {
+        if constexpr (R >= 16) return row * R + (piece ^ (row & 15));
+        return (row * R + piece) ^ (((row >> 2) & 1) << 3 | ((row >> 3) & 1) << 2);
     }
-    // piece kk of row i0 + l % 16 of a tile
-    static __device__ __forceinline__ i32x4 row(const T* t, int pitch, int i0, int kk) {
-        const int l = lane_id();
-        return *(const i32x4*)(t + (i0 + (l & 15)) * pitch + (kk * 4 + (l >> 4)) * E16);
+}
+
+// Through a buffer descriptor: lanes outside of it load zeros and store nothing.
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ i32x4 load16(__amdgpu_buffer_rsrc_t t, int offset) {
+    return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(t, offset, 0, 0));
+}
+__device__ __forceinline__ void store16(__amdgpu_buffer_rsrc_t t, int offset, const i32x4& v) {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), t, offset, 0, 0);
+}
+template <typename T>
+__device__ __forceinline__ typename Raw4<T>::t load4(__amdgpu_buffer_rsrc_t t, int offset) {
+    if constexpr (sizeof(T) == 2) return __builtin_bit_cast(bf16x4, __builtin_amdgcn_raw_buffer_load_b64(t, offset, 0, 0));
+    else return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(t, offset, 0, 0));
+}
+template <typename T>
+__device__ __forceinline__ void put4(__amdgpu_buffer_rsrc_t t, int offset, const f32x4& v) {
+    if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, Raw4<bf16>::narrow(v)), t, offset, 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), t, offset, 0, 0);
+}
+__device__ __forceinline__ float uniform(float x) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, x)));
+}
+
+// A wave-uniform value whose uses are not computed ahead of the loop they stand in (registers decide how many workgroups a
+// compute unit holds).
+__device__ __forceinline__ int fresh(int x) {
+    asm volatile("" : "+s"(x));
+    return x;
+}
+
+// The rows of one tensor, chunk by chunk.  A chunk is reached through a buffer descriptor that starts at its lowest row and
+// ends behind its highest, so the rows that a last chunk lacks lie outside of it (against time below it, at offsets that
+// wrap): they load as zeros and are not stored, without a branch.
+struct DlaStream {
+    const char* p;          // the lowest row of the next chunk, if it were whole
+    long step;
+    int whole, part, lack;  // bytes of a whole and of the sequence's last chunk, and those the latter lacks below
+    int end, last;          // chunks from `end` on are not touched
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t next(int ch, int& shift) {
+        shift = ch == last ? lack : 0;
+        const int bytes = ch == last ? part : whole;
+        const char* at = p + shift;
+        p += step;
+        return __builtin_amdgcn_make_buffer_rsrc((void*)at, 0, ch < end ? bytes : 0, 0x27000);
     }
 };
 
+// A workgroup's share: VS columns of one pass of one chain, chunks c0 .. c1 - 1 of the sequence.  Row r of chunk ch is
+// token 64 ch + r, or L - 1 - (64 ch + r) against time.
 template <typename T, int K, int VS, bool LOCAL>
-__global__ __launch_bounds__(kDlaThreads) void gdr2_dla_kernel(DlaParams p, int V, int nwork) {
-    using W = Dla<T, K, VS>;
-    constexpr int ES = W::ES, E16 = W::E16, KP = W::KP, KB = W::KB, VB = W::VB, PY = W::PY, PZ = W::PZ;
-    __shared__ __align__(16) T Yl[2][C * PY];
-    __shared__ __align__(16) T Zl[2][C * PZ];
-    __shared__ __align__(16) T Sl[LOCAL ? 1 : 2][LOCAL ? 8 : VS * PY];
+struct DlaWork {
+    static constexpr int ES = (int)sizeof(T), E16 = 16 / ES;     // elements of a 16-byte piece
+    static constexpr int RY = K * ES / 16, RZ = VS * ES / 16;    // pieces of a row
+    const DlaParams& p;
+    const DlaPass& ps;
+    int V, slices, sl, ip, sg, h, b;
+    int L, nch, c0, c1;
+    float ga;
+    bool rev;
+    int early;              // against time the state before the first token is undecayed at it: one power less, once
+    int sx, sz;             // bytes from row to row (H <= 32768: 64 rows fit 32 bits)
 
-    // work items: slices of a chain's columns next to each other, then passes, segments, heads, sequences;
-    // neighbours, which read the same rows, run on one XCD
-    const int per = gridDim.x / 8, item = blockIdx.x % 8 * per + blockIdx.x / 8;
-    if (item >= nwork) return;
-    const int slices = V / VS, segs = LOCAL ? p.segs - 1 : p.segs;
-    const int sl = item % slices, ip = item / slices % p.passes, sg = item / slices / p.passes % segs;
-    const int bh = item / slices / p.passes / segs, h = bh % p.H, b = bh / p.H;
-    const DlaPass& ps = p.pass[ip];
-    const int l = lane_id(), w = __builtin_amdgcn_readfirstlane(wave_id()), c = l & 15, g = l >> 4, tid = threadIdx.x;
+    // Slices of a chain's columns lie next to each other, then passes, segments, heads, sequences: neighbours, which read
+    // the same rows, run on one XCD.
+    __device__ __forceinline__ DlaWork(const DlaParams& q, int width, int item)
+        : p(q), ps(q.pass[item / (width / VS) % q.passes]), V(width), slices(width / VS) {
+        const int segs = LOCAL ? p.segs - 1 : p.segs;
+        sl = item % slices, ip = item / slices % p.passes, sg = item / slices / p.passes % segs;
+        const int bh = item / slices / p.passes / segs;
+        h = bh % p.H, b = bh / p.H;
+        const int n = p.lengths ? p.lengths[b] : p.T;
+        L = __builtin_amdgcn_readfirstlane(n < 0 ? 0 : n > p.T ? p.T : n);  // wave-uniform, for the descriptors
+        nch = (L + C - 1) / C, c0 = sg * p.seg_chunks;
+        c1 = c0 + p.seg_chunks < nch ? c0 + p.seg_chunks : nch;
+        ga = uniform(p.log_decay[h]);
+        rev = ps.reverse;
+        early = rev ? 1 : 0;
+        sx = p.H * K * ES, sz = p.H * V * ES;
+    }
+    __device__ __forceinline__ int off(int r, int stride) const { return (rev ? C - 1 - r : r) * stride; }
+    __device__ __forceinline__ DlaStream stream(const void* t, int stride, int bytes, int width, int col) const {
+        const long low = (long)b * p.T + (rev ? (long)L - (c0 + 1) * C : (long)c0 * C);
+        const int tail = L - (nch - 1) * C;  // rows of the sequence's last chunk
+        return DlaStream{(const char*)t + ((low * p.H + h) * width + col) * ES, (long)(rev ? -C : C) * stride, (C - 1) * stride + bytes,
+                         (tail - 1) * stride + bytes, rev ? (C - tail) * stride : 0, c1, nch - 1};
+    }
+    __device__ __forceinline__ DlaStream rows_of_k(const void* t) const { return stream(t, sx, K * ES, K, 0); }
+    __device__ __forceinline__ DlaStream rows_of_v(const void* t) const { return stream(t, sz, VS * ES, V, sl * VS); }
+    // the number (k, column v of the slice) of the chain's state in memory
+    __device__ __forceinline__ long state_at(int k, int v) const {
+        return ((long)b * p.H + h) * K * V + (ps.flip ? (long)(sl * VS + v) * K + k : (long)k * V + sl * VS + v);
+    }
+    // the own state of segment j
+    __device__ __forceinline__ float* local(int j) const {
+        return p.local + (((((long)ip * p.B + b) * p.H + h) * (p.segs - 1) + j) * slices + sl) * (K * VS);
+    }
+    __device__ __forceinline__ bool final_here() const { return nch == 0 ? sg == 0 : c0 < nch && c1 == nch; }
+    // the state's decay over chunk ch less one: S <- S + S (a^n - 1)
+    __device__ __forceinline__ float decay(int ch, float whole) const {
+        const int n = L - ch * C < C ? L - ch * C : C, m = n - (ch == 0 ? early : 0);
+        return m == C ? whole : m == 0 ? 0.f : expm1f((float)m * ga);
+    }
+    // zeros behind the sequence, in the segment's part of the time axis
+    __device__ __forceinline__ void pad(int tid, int threads) const {
+        const long t0 = L > (long)c0 * C ? L : (long)c0 * C, t1 = sg + 1 < p.segs ? (long)(c0 + p.seg_chunks) * C : p.T;
+        char* out = (char*)ps.out + ((((long)b * p.T) * p.H + h) * V + sl * VS) * ES;
+        for (long x = tid; x < (t1 - t0) * RZ; x += threads)
+            *(i32x4*)(out + (t0 + x / RZ) * p.H * V * ES + x % RZ * 16) = i32x4{0, 0, 0, 0};
+    }
+};
 
-    int L = p.lengths ? p.lengths[b] : p.T;
-    L = L < 0 ? 0 : L > p.T ? p.T : L;
-    const int nch = (L + C - 1) / C, c0 = sg * p.seg_chunks;
-    const int c1 = c0 + p.seg_chunks < nch ? c0 + p.seg_chunks : nch;
-    if (LOCAL && c1 - c0 < p.seg_chunks) return;  // no later segment has a token: nobody reads this one's state
-    const float ga = p.log_decay[h];
-    const bool rev = ps.reverse;
-
-    // rows: token t of the pass is row t, or L - 1 - t against time
-    const long sx = (long)p.H * K * ES * (rev ? -1 : 1), sz = (long)p.H * V * ES * (rev ? -1 : 1);
-    const long row0 = ((long)b * p.T + (rev ? L - 1 : 0)) * p.H + h;
-    const char* X = (const char*)ps.x + row0 * K * ES;
-    const char* Y = (const char*)ps.y + row0 * K * ES;
-    const char* Z = (const char*)ps.z + (row0 * V + sl * VS) * ES;
-    char* O = (char*)ps.out + (row0 * V + sl * VS) * ES;
-
-    // The state: blocks of 16 x 16, rows k = 16 (w + 4 kb) + 4 g + i, columns v = 16 vb + c
-    f32x4 S[KB][VB];
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-        for (int vb = 0; vb < VB; ++vb) S[kb][vb] = f32x4{0, 0, 0, 0};
-    const int tsl = KB * VB * kDlaThreads * 4;  // numbers of a slice's state
-    const long chain = ((long)ip * p.B + b) * p.H + h;
-    auto each_state = [&](auto&& f) {
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-            for (int vb = 0; vb < VB; ++vb)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int k = 16 * (w + 4 * kb) + 4 * g + i, v = sl * VS + 16 * vb + c;
-                    f(S[kb][vb], i, ((long)b * p.H + h) * K * V + (ps.flip ? (long)v * K + k : (long)k * V + v));
-                }
+// Staging of y (16 bytes at a time, by NY threads) and z (four columns at a time, by NZ), z also as the decayed operand
+// z_s a^(63 - s) of the state's sums: for bf16 in parts of 8 bits each, three where the state is a result, two where it is only
+// read as bf16.  With two buffers (NB) set (ch - c0) % 2 of the
+// registers and of the tiles belongs to chunk ch.  Behind the last chunk nothing is loaded.
+template <typename T, int K, int VS, bool LOCAL, int NY, int NZ, int NB>
+struct DlaStage {
+    typedef DlaWork<T, K, VS, LOCAL> Work;
+    typedef typename Raw4<T>::t z4;
+    static constexpr int ES = Work::ES, E16 = Work::E16, RY = Work::RY, RZ = Work::RZ;
+    static constexpr int YU = C * RY / NY, ZU = C * VS / 4 / NZ, NP = ES == 2 ? 3 : 1;
+    static constexpr int RS = ES == 2 ? RY + 1 : RY;  // pieces of a row of the state (bf16: read along rows only, padded by one)
+    static_assert(YU >= 1 && ZU >= 1, "staging");
+    struct Tiles {
+        i32x4 y[NB][C * RY];
+        i32x4 z[LOCAL ? 1 : NB][LOCAL ? 1 : C * RZ];
+        i32x4 d[NB][NP][C * RZ];
+        i32x4 s[LOCAL ? 1 : NB][LOCAL ? 1 : VS * RS];  // the state as the chunk reads it, [v][k]
     };
-    // Against time the state before the first token is undecayed at that token: one power less (in the first chunk).
-    const int early = rev ? 1 : 0;
-    if constexpr (!LOCAL) {
-        if (ps.init) each_state([&](f32x4& s, int i, long at) { s[i] = ps.init[at]; });
-        for (int j = 0; j < sg; ++j) {
-            if (c0 >= nch && sg > 0) break;  // no token here
-            const float e = expm1f((float)(p.seg_chunks * C - (j == 0 ? early : 0)) * ga);
-            const f32x4* src = (const f32x4*)(p.local + ((chain * (p.segs - 1) + j) * slices + sl) * tsl) + tid;
+    const Work& k;
+    Tiles& t;
+    DlaStream ys, zs;
+    i32x4 yr[NB][YU];
+    z4 zr[NB][ZU];
+    int yt, zt, yo[YU], zo[ZU];
+    float late[ZU];  // a^(63 - s) of the staged rows
+    bool exact;      // the third part too
+    __device__ __forceinline__ DlaStage(const Work& work, Tiles& tiles, int ythread, int zthread)
+        : k(work), t(tiles), ys(work.rows_of_k(work.ps.y)), zs(work.rows_of_v(work.ps.z)), yt(ythread), zt(zthread), exact(LOCAL || (work.ps.state && work.final_here())) {
+#pragma unroll
+        for (int u = 0; u < YU; ++u) yo[u] = k.off((yt + u * NY) / RY, k.sx) + (yt + u * NY) % RY * 16;
+#pragma unroll
+        for (int u = 0; u < ZU; ++u) {
+            const int x = zt + u * NZ, r = x / (VS / 4);
+            zo[u] = k.off(r, k.sz) + x % (VS / 4) * 4 * ES;
+            late[u] = dla_pow(k.ga, C - 1 - r);
+        }
+    }
+    template <int P>
+    __device__ __forceinline__ void fetch_y(int ch) {
+        int shift;
+        const auto y = ys.next(ch, shift);
+#pragma unroll
+        for (int u = 0; u < YU; ++u) yr[P][u] = load16(y, yo[u] - shift);
+    }
+    template <int P>
+    __device__ __forceinline__ void fetch_z(int ch) {
+        int shift;
+        const auto z = zs.next(ch, shift);
+#pragma unroll
+        for (int u = 0; u < ZU; ++u) zr[P][u] = load4<T>(z, zo[u] - shift);
+    }
+    template <int P>
+    __device__ __forceinline__ void put_y() {
+#pragma unroll
+        for (int u = 0; u < YU; ++u) t.y[P][tile_at<T, RY>((yt + u * NY) / RY, (yt + u * NY) % RY)] = yr[P][u];
+    }
+    template <int P>
+    __device__ __forceinline__ void put_z(int ch) {
+        const int n = k.L - ch * C;
+#pragma unroll
+        for (int u = 0; u < ZU; ++u) {
+            const int x = zt + u * NZ, r = x / (VS / 4), col = x % (VS / 4) * 4;
+            const int at = tile_at<T, RZ>(r, col / E16), in = col % E16;
+            if constexpr (!LOCAL) *(z4*)((T*)(t.z[P] + at) + in) = zr[P][u];
+            const float f = n >= C ? late[u] : r < n ? dla_pow(k.ga, n - 1 - r) : 0.f;
+            f32x4 rest = Raw4<T>::widen(zr[P][u]) * f;
+            if constexpr (ES == 2) {
+                // each time the upper eight bits of what is left: after three nothing remains of 24
+#pragma unroll
+                for (int q = 0; q < NP; ++q) {
+                    if (q == 2 && !exact) break;
+                    u32x2 part;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float even = rest[2 * i], odd = rest[2 * i + 1];
+                        const unsigned lo = __builtin_bit_cast(unsigned, even), hi = __builtin_bit_cast(unsigned, odd);
+                        part[i] = __builtin_amdgcn_perm(hi, lo, 0x07060302);
+                        rest[2 * i] = even - __builtin_bit_cast(float, lo & 0xffff0000u);
+                        rest[2 * i + 1] = odd - __builtin_bit_cast(float, hi & 0xffff0000u);
+                    }
+                    *(u32x2*)((T*)(t.d[P][q] + at) + in) = part;
+                }
+            } else {
+                *(f32x4*)(t.d[P][0] + at) = rest;
+            }
+        }
+    }
+    template <int P>
+    __device__ __forceinline__ void fetch(int ch) {
+        fetch_y<P>(ch);
+        fetch_z<P>(ch);
+    }
+    template <int P>
+    __device__ __forceinline__ void put(int ch) {
+        put_y<P>();
+        put_z<P>(ch);
+    }
+};
+
+// The workgroup's place in the launch; -1: none.
+__device__ __forceinline__ int dla_item(int nwork) {
+    const int per = gridDim.x / 8, item = blockIdx.x % 8 * per + blockIdx.x / 8;
+    return item < nwork ? item : -1;
+}
+
+// ------------------------------------------------------------------ bf16
+// 32 x 32 products over 64 columns.  Two waves read: outputs of 32 rows each.  Two carry the state: every other 32 of its
+// rows.  They run loops of their own that meet at two barriers per chunk, before and behind the products; between the second
+// and the next first the next chunk's tiles are written.  (For a segment's own state alone, LOCAL, all four carry.)
+__device__ __forceinline__ int acc_row32(int i, int l) { return 8 * (i / 4) + 4 * (l >> 5) + i % 4; }
+// operand of 32 columns from piece q of a tile, contraction down sixteen rows from r0: rows 4 h .. + 3 and 8 + 4 h .. + 3
+template <int R>
+__device__ __forceinline__ bf16x8 columns32(const i32x4* t, int r0, int q, int l) {
+    const int p = l & 15, row = r0 + 4 * (l >> 5) + (p >> 2), piece = q + 2 * ((l >> 4) & 1) + ((p & 3) >> 1);
+    const bf16x4 lo = ds_read_tr4((const bf16*)(t + tile_at<bf16, R>(row, piece)) + 4 * (p & 1));
+    const bf16x4 hi = ds_read_tr4((const bf16*)(t + tile_at<bf16, R>(row + 8, piece)) + 4 * (p & 1));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+__device__ __forceinline__ void mma32x32(f32x16& c, const bf16x8& a, const bf16x8& b) {
+    c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 zeros16() { return f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0}; }
+
+template <int K, bool LOCAL>
+__global__ __launch_bounds__(256, LOCAL ? 3 : 2) void gdr2_dla_kernel(DlaParams p, int V, int nwork) {
+    typedef DlaWork<bf16, K, kDlaVS, LOCAL> Work;
+    typedef DlaStage<bf16, K, kDlaVS, LOCAL, LOCAL ? 256 : 128, 256, 1> Stage;
+    constexpr int KK = K / 16, RY = Work::RY, RZ = Work::RZ, VB = kDlaVS / 32;
+    // carrying waves, and the blocks of 32 x 32 of each: rows cw % NK + NK kb, columns cv + vb (times 32)
+    constexpr int NW = LOCAL ? 4 : 2, NK = NW < K / 32 ? NW : K / 32, KB = K / 32 / NK, CB = VB * NK / NW;
+    __shared__ typename Stage::Tiles t;
+    __shared__ i32x4 Xl[LOCAL ? 1 : 2][32 * 9];  // a reading wave's own: 64 channels of its rows, or its outputs
+    const int item = dla_item(nwork);
+    if (item < 0) return;
+    const Work k(p, V, item);
+    if (LOCAL && k.c1 - k.c0 < p.seg_chunks) return;  // no later segment has a token: nobody reads this one's state
+    const int l = lane_id(), w = __builtin_amdgcn_readfirstlane(wave_id()), n = l & 31, hf = l >> 5;
+    Stage st(k, t, (int)threadIdx.x - (LOCAL ? 0 : 128), threadIdx.x);
+    if (LOCAL || w >= 2) {
+        const int cw = LOCAL ? w : w - 2, ck = cw % NK, cv = cw / NK * CB;
+        f32x16 S[KB][CB];  // rows 32 (ck + NK kb) + acc_row32(i), columns 32 (cv + vb) + n
+        auto each_block = [&](auto&& f) {
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-                for (int vb = 0; vb < VB; ++vb) {
-                    const f32x4 x = src[(kb * VB + vb) * kDlaThreads];
+                for (int vb = 0; vb < CB; ++vb) f(S[kb][vb], ck + NK * kb, cv + vb);
+        };
+        auto each_four = [&](int j, auto&& f) {  // of the own state of segment j
+            f32x4* at = (f32x4*)k.local(j) + l;
+            each_block([&](f32x16& s, int kb, int vb) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) S[kb][vb][i] = fmaf(S[kb][vb][i], e, S[kb][vb][i]) + x[i];
-                }
+                for (int i = 0; i < 4; ++i) f(s, 4 * i, at[((kb * VB + vb) * 4 + i) * 64]);
+            });
+        };
+        each_block([&](f32x16& s, int, int) { s = zeros16(); });
+        if constexpr (!LOCAL) {
+            if (k.ps.init)
+                each_block([&](f32x16& s, int kb, int vb) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) s[i] = k.ps.init[k.state_at(32 * kb + acc_row32(i, l), 32 * vb + n)];
+                });
+            for (int j = 0; j < k.sg && k.c0 < k.nch; ++j) {
+                const float e = expm1f((float)(p.seg_chunks * C - (j == 0 ? k.early : 0)) * k.ga);
+                each_four(j, [&](f32x16& s, int i0, const f32x4& x) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[i0 + i] = fmaf(s[i0 + i], e, s[i0 + i]) + x[i];
+                });
+            }
         }
+        auto put_state = [&]() {
+            if constexpr (!LOCAL)
+                each_block([&](const f32x16& s, int kb, int vb) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        store4((bf16*)(t.s[0] + (32 * vb + n) * Stage::RS + 4 * kb + i) + 4 * hf, f32x4{s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]});
+                });
+        };
+        const float whole = expm1f((float)C * k.ga);
+        if (k.c0 < k.c1) {
+            st.template fetch<0>(k.c0);
+            put_state();
+            st.template put<0>(k.c0);
+            st.template fetch<0>(k.c0 + 1);
+        }
+        for (int ch = k.c0; ch < k.c1; ++ch) {
+            lds_barrier();
+            const float e = k.decay(ch, whole);
+            each_block([&](f32x16& s, int, int) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[i] = fmaf(s[i], e, s[i]);
+            });
+#pragma unroll
+            for (int kk = 0; kk < C / 16; ++kk) {
+                bf16x8 y[KB];
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) y[kb] = columns32<RY>(t.y[0], 16 * kk, 4 * (ck + NK * kb), l);
+#pragma unroll
+                for (int q = 0; q < Stage::NP; ++q) {
+                    if (q == 2 && !st.exact) break;
+#pragma unroll
+                    for (int vb = 0; vb < CB; ++vb) {
+                        const bf16x8 z = columns32<RZ>(t.d[0][q], 16 * kk, 4 * (cv + vb), l);
+#pragma unroll
+                        for (int kb = 0; kb < KB; ++kb) mma32x32(S[kb][vb], y[kb], z);
+                    }
+                }
+            }
+            if (ch + 1 < k.c1) {
+                lds_barrier();
+                put_state();
+                st.template put<0>(ch + 1);
+                st.template fetch<0>(ch + 2);
+            }
+        }
+        if constexpr (LOCAL) {
+            each_four(k.sg, [&](const f32x16& s, int i0, f32x4& x) { x = f32x4{s[i0], s[i0 + 1], s[i0 + 2], s[i0 + 3]}; });
+        } else if (k.ps.fin && k.final_here()) {
+            // against time the final state is decayed once more (dS0 = a R_0)
+            const float f = k.rev && k.L > 0 ? dla_pow(k.ga, 1) : 1.f;
+            each_block([&](const f32x16& s, int kb, int vb) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) k.ps.fin[k.state_at(32 * kb + acc_row32(i, l), 32 * vb + n)] = s[i] * f;
+            });
+        }
+    } else {
+        // The wave's 32 rows arrive as whole lines (a lane's own pieces, as the products want them, would be 32 lines a
+        // load), and outputs leave so; both turn round in the wave's own LDS.
+        DlaStream xs = k.rows_of_k(k.ps.x), os = k.rows_of_v(k.ps.out);
+        i32x4* own = Xl[w];
+        constexpr int XR = 8, XH = K / 64;  // pieces of a row and rounds: 64 channels at a time
+        const int xrow = 32 * w + n;
+        const int xo = k.off(32 * w + l / XR, k.sx) + l % XR * 16, oo = k.off(32 * w + l / RZ, k.sz) + l % RZ * 16;
+        const int xd = k.rev ? -8 * k.sx : 8 * k.sx, od = k.rev ? -8 * k.sz : 8 * k.sz;  // eight rows on
+        int at[KK];  // row n of a tile, the lane's piece
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) at[kk] = tile_at<bf16, RY>(n, 2 * kk + hf);
+        i32x4 xp[XH][4], xr[KK];
+        auto fetch_x = [&](int ch) {
+            int shift;
+            const auto x = xs.next(ch, shift);
+#pragma unroll
+            for (int q = 0; q < XH; ++q)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) xp[q][u] = load16(x, xo + (xd * u - shift) + q * 128);
+        };
+        auto take_x = [&]() {
+#pragma unroll
+            for (int q = 0; q < XH; ++q) {
+                wave_sync();
+#pragma unroll
+                for (int u = 0; u < 4; ++u) own[(8 * u + l / XR) * (XR + 1) + l % XR] = xp[q][u];
+                wave_sync();
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) xr[4 * q + kk] = own[n * (XR + 1) + 2 * kk + hf];
+            }
+        };
+        auto put_out = [&](int ch, const f32x16 (&out)[VB]) {
+            static_assert(RZ == XR, "outputs turn round in the rows' place");
+            wave_sync();
+#pragma unroll
+            for (int vb = 0; vb < VB; ++vb)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    store4((bf16*)(own + n * (XR + 1) + 4 * vb + i) + 4 * hf, f32x4{out[vb][4 * i], out[vb][4 * i + 1], out[vb][4 * i + 2], out[vb][4 * i + 3]});
+            wave_sync();
+            int shift;
+            const auto o = os.next(ch, shift);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) store16(o, oo + (od * u - shift), own[(8 * u + l / XR) * (XR + 1) + l % XR]);
+        };
+        // Weights that every chunk shares: a^(r - s) inside the wave's 32 rows and to the 32 before them.  The lane's values
+        // 4 j .. 4 j + 3 of a block are rows s = s_j .. s_j + 3, so a^(r - s) is a^(r - s_j - 3) times a^3, a^2, a, 1; both are
+        // powers with an exponent >= 0 but where the diagonal passes through the four, which have weights of their own.
+        float self[4], prev[4], diag[4];
+        const float a1 = uniform(dla_pow(k.ga, 1)), a2 = uniform(dla_pow(k.ga, 2)), a3 = uniform(dla_pow(k.ga, 3));
+        const float fall[4] = {a3, a2, a1, 1.f};
+        const int first = n - 4 * hf;     // r - s_0
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            self[j] = first - 8 * j < 3 ? 0.f : dla_pow(k.ga, first - 8 * j - 3);
+            prev[j] = dla_pow(k.ga, first - 8 * j + 29);
+            const int lag = (n & 7) - 4 * hf - j;
+            diag[j] = lag < 0 ? 0.f : dla_pow(k.ga, lag);
+        }
+        const int on = first < 0 || first % 8 > 2 ? -1 : first / 8;  // the four that the diagonal leaves in part
+        const float before = dla_pow(k.ga, xrow + 1), before0 = k.early ? dla_pow(k.ga, xrow) : before;
+        if (k.c0 < k.c1) {
+            fetch_x(k.c0);
+            st.template fetch_z<0>(k.c0);
+            take_x();
+            st.template put_z<0>(k.c0);
+            fetch_x(k.c0 + 1);
+            st.template fetch_z<0>(k.c0 + 1);
+        }
+        for (int ch = k.c0; ch < k.c1; ++ch) {
+            lds_barrier();
+            // from before the chunk: out^T = S^T x, rows v, columns r; and scores, rows s, columns r
+            f32x16 out[VB], sc = zeros16();
+#pragma unroll
+            for (int vb = 0; vb < VB; ++vb) out[vb] = zeros16();
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk) {
+                const bf16x8 x = __builtin_bit_cast(bf16x8, xr[kk]);
+                mma32x32(sc, __builtin_bit_cast(bf16x8, t.y[0][at[kk] + w * 32 * RY]), x);
+#pragma unroll
+                for (int vb = 0; vb < VB; ++vb)
+                    mma32x32(out[vb], __builtin_bit_cast(bf16x8, t.s[0][(32 * vb + n) * Stage::RS + 2 * kk + hf]), x);
+            }
+            const float f = ch == 0 ? before0 : before;
+#pragma unroll
+            for (int vb = 0; vb < VB; ++vb)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) out[vb][i] *= f;
+            // out^T += z^T scores^T
+            auto add = [&](const f32x16& score, int r0, auto inside) {
+                constexpr bool SELF = decltype(inside)::value;
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) {
+                    bf16x8 pr;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int j = 2 * kk + e / 4, i = e % 4;
+                        const float wt = SELF ? j == on ? diag[i] : self[j] * fall[i] : prev[j] * fall[i];
+                        pr[e] = (bf16)(score[8 * kk + e] * wt);
+                    }
+#pragma unroll
+                    for (int vb = 0; vb < VB; ++vb) mma32x32(out[vb], columns32<RZ>(t.z[0], r0 + 16 * kk, 4 * vb, l), pr);
+                }
+            };
+            add(sc, 32 * w, IC<1>{});
+            if (w) {
+                sc = zeros16();
+#pragma unroll
+                for (int kk = 0; kk < KK; ++kk)
+                    mma32x32(sc, __builtin_bit_cast(bf16x8, t.y[0][at[kk]]), __builtin_bit_cast(bf16x8, xr[kk]));
+                add(sc, 0, IC<0>{});
+            }
+            put_out(ch, out);
+            if (ch + 1 < k.c1) {
+                take_x();
+                fetch_x(ch + 2);
+                lds_barrier();
+                st.template put_z<0>(ch + 1);
+                st.template fetch_z<0>(ch + 2);
+            }
+        }
+        k.pad(threadIdx.x, 128);
     }
-    auto put_state = [&](T* dst) {  // as read by the next chunk: [v][k]
+}
+
+// ------------------------------------------------------------------ fp32
+// 16 x 16 products, of which this type's scores need eight times as many cycles: waves 0..3 read sixteen rows each,
+// waves 4..7 carry every fourth sixteen of the state's rows.
+template <int K, bool LOCAL>
+__global__ __launch_bounds__(LOCAL ? 256 : 512, 2) void gdr2_dla_f32_kernel(DlaParams p, int V, int nwork) {
+    constexpr int NT = LOCAL ? 256 : 512;
+    typedef DlaWork<float, K, kDlaF32VS, LOCAL> Work;
+    typedef DlaStage<float, K, kDlaF32VS, LOCAL, NT, NT, 2> Stage;
+    constexpr int KP = K / 16, KB = K / 64, VB = kDlaF32VS / 16, RY = Work::RY, RZ = Work::RZ;
+    __shared__ typename Stage::Tiles t;
+    const int item = dla_item(nwork);
+    if (item < 0) return;
+    const Work k(p, V, item);
+    if (LOCAL && k.c1 - k.c0 < p.seg_chunks) return;
+    const int l = lane_id(), w = __builtin_amdgcn_readfirstlane(wave_id()), c = l & 15, g = l >> 4;
+    // operand value of column 16 block + l % 16, contraction down the rows
+    auto column = [&](const i32x4* tile, auto pieces, int row, int block) {
+        constexpr int R = decltype(pieces)::value;
+        return ((const float*)(tile + tile_at<float, R>(row, 4 * block + (c >> 2))))[c & 3];
+    };
+    Stage st(k, t, threadIdx.x, threadIdx.x);
+    if (k.c0 < k.c1) {
+        st.template fetch<0>(k.c0);
+        st.template fetch<1>(k.c0 + 1);
+    }
+    if (LOCAL || w >= 4) {
+        // blocks of 16 x 16: rows 16 (cw + 4 kb) + 4 g + i, column 16 vb + c
+        const int cw = LOCAL ? w : w - 4;
+        f32x4 S[KB][VB];
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-            for (int vb = 0; vb < VB; ++vb) store4(dst + (16 * vb + c) * PY + 16 * (w + 4 * kb) + 4 * g, S[kb][vb]);
-    };
-
-    // staging: piece u of a thread is row (tid + 256 u) / pieces of a row
-    constexpr int YR = K * ES / 16, ZR = VS * ES / 16;
-    i32x4 yr[W::YU], zr[W::ZU], xr[KP];
-    const int xrow = 16 * w + c;
-    auto fetch = [&](int ch) {
-        const int n = L - ch * C;
+            for (int vb = 0; vb < VB; ++vb) S[kb][vb] = f32x4{0, 0, 0, 0};
+        auto each = [&](auto&& f) {
 #pragma unroll
-        for (int u = 0; u < W::YU; ++u) {
-            const int x = tid + u * kDlaThreads, r = x / YR, q = x % YR;
-            yr[u] = r < n ? *(const i32x4*)(Y + (ch * C + r) * sx + q * 16) : i32x4{0, 0, 0, 0};
-        }
+            for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-        for (int u = 0; u < W::ZU; ++u) {
-            const int x = tid + u * kDlaThreads, r = x / ZR, q = x % ZR;
-            zr[u] = r < n ? *(const i32x4*)(Z + (ch * C + r) * sz + q * 16) : i32x4{0, 0, 0, 0};
-        }
+                for (int vb = 0; vb < VB; ++vb) f(S[kb][vb], 16 * (cw + 4 * kb) + 4 * g, 16 * vb + c, (kb * VB + vb) * 256 + cw * 64 + l);
+        };
         if constexpr (!LOCAL) {
+            if (k.ps.init)
+                each([&](f32x4& s, int row, int v, int) {
 #pragma unroll
-            for (int kk = 0; kk < KP; ++kk)
-                xr[kk] = xrow < n ? *(const i32x4*)(X + (ch * C + xrow) * sx + (kk * 4 + g) * 16) : i32x4{0, 0, 0, 0};
+                    for (int i = 0; i < 4; ++i) s[i] = k.ps.init[k.state_at(row + i, v)];
+                });
+            for (int j = 0; j < k.sg && k.c0 < k.nch; ++j) {
+                const float e = expm1f((float)(p.seg_chunks * C - (j == 0 ? k.early : 0)) * k.ga);
+                const f32x4* own = (const f32x4*)k.local(j);
+                each([&](f32x4& s, int, int, int at) {
+                    const f32x4 x = own[at];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[i] = fmaf(s[i], e, s[i]) + x[i];
+                });
+            }
         }
-    };
-    auto stage = [&](int buf) {
-#pragma unroll
-        for (int u = 0; u < W::YU; ++u) {
-            const int x = tid + u * kDlaThreads, r = x / YR, q = x % YR;
-            *(i32x4*)(Yl[buf] + r * PY + q * E16) = yr[u];
+        auto put_state = [&](auto set) {
+            constexpr int P = decltype(set)::value;
+            if constexpr (!LOCAL) each([&](const f32x4& s, int row, int v, int) { *(f32x4*)(t.s[P] + tile_at<float, RY>(v, row / 4)) = s; });
+        };
+        const float whole = expm1f((float)C * k.ga);
+        if (k.c0 < k.c1) {
+            put_state(IC<0>{});
+            st.template put<0>(k.c0);
+            st.template fetch<0>(k.c0 + 2);
         }
+        auto chunk = [&](int ch, auto set) {
+            constexpr int P = decltype(set)::value;
+            lds_barrier();
+            const float e = k.decay(ch, whole);
+            each([&](f32x4& s, int, int, int) {
 #pragma unroll
-        for (int u = 0; u < W::ZU; ++u) {
-            const int x = tid + u * kDlaThreads, r = x / ZR, q = x % ZR;
-            *(i32x4*)(Zl[buf] + r * PZ + q * E16) = zr[u];
+                for (int i = 0; i < 4; ++i) s[i] = fmaf(s[i], e, s[i]);
+            });
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const int r = 16 * (j / 4) + 4 * g + j % 4;
+                float y[KB];
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) y[kb] = column(t.y[P], IC<RY>{}, r, cw + 4 * kb);
+#pragma unroll
+                for (int vb = 0; vb < VB; ++vb) {
+                    const float z = column(t.d[P][0], IC<RZ>{}, r, vb);
+#pragma unroll
+                    for (int kb = 0; kb < KB; ++kb) mma32(S[kb][vb], y[kb], z);
+                }
+            }
+            if (ch + 1 < k.c1) {
+                put_state(IC<1 - P>{});
+                st.template put<1 - P>(ch + 1);
+            }
+            st.template fetch<1 - P>(ch + 3);
+        };
+        for (int ch = k.c0; ch < k.c1; ch += 2) {
+            chunk(ch, IC<0>{});
+            if (ch + 1 < k.c1) chunk(ch + 1, IC<1>{});
         }
-    };
-
-    // weights that every chunk shares: near[b][i] = a^(r - s) of score block b, late[j] = a^(63 - s)
-    float near[4][4], late[16];
+        if constexpr (LOCAL) {
+            f32x4* own = (f32x4*)k.local(k.sg);
+            each([&](const f32x4& s, int, int, int at) { own[at] = s; });
+        } else if (k.ps.fin && k.final_here()) {
+            const float f = k.rev && k.L > 0 ? dla_pow(k.ga, 1) : 1.f;
+            each([&](const f32x4& s, int row, int v, int) {
 #pragma unroll
-    for (int sb = 0; sb < 4; ++sb)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int lag = xrow - (16 * sb + 4 * g + i);
-            near[sb][i] = lag < 0 ? 0.f : dla_pow(ga, lag);
+                for (int i = 0; i < 4; ++i) k.ps.fin[k.state_at(row + i, v)] = s[i] * f;
+            });
         }
-    // token of the lane's contraction value j of the state's products
-    auto late_token = [&](int j) { return ES == 2 ? 32 * (j / 8) + 8 * g + j % 8 : 4 * j + g; };
+    } else {
+        DlaStream xs = k.rows_of_k(k.ps.x), os = k.rows_of_v(k.ps.out);
+        const int xrow = 16 * w + c, xo = k.off(xrow, k.sx) + g * 16, oo = k.off(xrow, k.sz) + g * 16;
+        i32x4 xr[2][KP];
+        auto fetch_x = [&](int ch, auto set) {
+            constexpr int P = decltype(set)::value;
+            int shift;
+            const auto x = xs.next(ch, shift);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) late[j] = dla_pow(ga, C - 1 - late_token(j));
-    float carry = expm1f((float)C * ga);
-
-    if (c0 < c1) {
-        fetch(c0);
-        stage(0);
-        if constexpr (!LOCAL) put_state(Sl[0]);
-    }
-    i32x4 xf[KP];
-    int buf = 0;
-    for (int ch = c0; ch < c1; ++ch, buf ^= 1) {
-        lds_barrier();
-        const int n = L - ch * C < C ? L - ch * C : C;
-        if constexpr (!LOCAL) {
+            for (int kk = 0; kk < KP; ++kk) xr[P][kk] = load16(x, xo - shift + kk * 64);
+        };
+        // products of 16 x 16 by sixteen values of contraction
+        auto mma = [&](f32x4& acc, const i32x4& a, const i32x4& b) {
+            const f32x4 x = __builtin_bit_cast(f32x4, a), y = __builtin_bit_cast(f32x4, b);
 #pragma unroll
-            for (int kk = 0; kk < KP; ++kk) xf[kk] = xr[kk];
+            for (int e = 0; e < 4; ++e) mma32(acc, x[e], y[e]);
+        };
+        // weights that every chunk shares: near[b][i] = a^(r - s) of score block b, before = a^(r + 1)
+        float near[4][4];
+#pragma unroll
+        for (int sb = 0; sb < 4; ++sb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int lag = xrow - (16 * sb + 4 * g + i);
+                near[sb][i] = lag < 0 ? 0.f : dla_pow(k.ga, lag);
+            }
+        const float before = dla_pow(k.ga, xrow + 1), before0 = k.early ? dla_pow(k.ga, xrow) : before;
+        if (k.c0 < k.c1) {
+            fetch_x(k.c0, IC<0>{});
+            fetch_x(k.c0 + 1, IC<1>{});
+            st.template put<0>(k.c0);
+            st.template fetch<0>(k.c0 + 2);
         }
-        if (ch + 1 < c1) fetch(ch + 1);
-        const T *yl = Yl[buf], *zl = Zl[buf];
-        if constexpr (!LOCAL) {
-            const T* st = Sl[buf];
-            // from before the chunk: out^T = S^T x, rows v, columns r
-            f32x4 out[VB];
+        auto chunk = [&](int ch, auto set) {
+            constexpr int P = decltype(set)::value;
+            lds_barrier();
+            f32x4 out[VB], sc[4];
 #pragma unroll
             for (int vb = 0; vb < VB; ++vb) out[vb] = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int kk = 0; kk < KP; ++kk)
 #pragma unroll
-                for (int vb = 0; vb < VB; ++vb) W::mma(out[vb], W::row(st, PY, 16 * vb, kk), xf[kk]);
-            const float before = dla_pow(ga, xrow + 1 - (ch == 0 ? early : 0));
+                for (int vb = 0; vb < VB; ++vb) mma(out[vb], t.s[P][tile_at<float, RY>(16 * vb + c, 4 * kk + g)], xr[P][kk]);
+            const float f = ch == 0 ? before0 : before;
 #pragma unroll
-            for (int vb = 0; vb < VB; ++vb) out[vb] *= before;
-            // scores, rows s, columns r; blocks behind the wave's rows are not seen
-            f32x4 sc[4];
+            for (int vb = 0; vb < VB; ++vb) out[vb] *= f;
+            // blocks of scores behind the wave's rows are not seen
 #pragma unroll
             for (int sb = 0; sb < 4; ++sb) {
-                sc[sb] = f32x4{0, 0, 0, 0};
                 if (sb <= w) {
+                    sc[sb] = f32x4{0, 0, 0, 0};
 #pragma unroll
-                    for (int kk = 0; kk < KP; ++kk) W::mma(sc[sb], W::row(yl, PY, 16 * sb, kk), xf[kk]);
+                    for (int kk = 0; kk < KP; ++kk) mma(sc[sb], t.y[P][tile_at<float, RY>(16 * sb + c, 4 * kk + g)], xr[P][kk]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sc[sb][i] = near[sb][i] == 0.f ? 0.f : sc[sb][i] * near[sb][i];
-                }
-            }
-            // out^T += z^T scores^T
-            if constexpr (ES == 2) {
+                    for (int i = 0; i < 4; ++i) {
+                        const float s = sc[sb][i] * near[sb][i];
 #pragma unroll
-                for (int kk = 0; kk < 2; ++kk) {
-                    if (2 * kk <= w) {
-                        bf16x8 pr;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) pr[e] = (bf16)sc[2 * kk][e], pr[4 + e] = (bf16)sc[2 * kk + 1][e];
-#pragma unroll
-                        for (int vb = 0; vb < VB; ++vb) {
-                            const T* a = zl + (32 * kk + 4 * g + (c >> 2)) * PZ + 16 * vb + 4 * (c & 3);
-                            const bf16x4 lo = ds_read_tr4(a), hi = ds_read_tr4(a + 16 * PZ);
-                            out[vb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7), pr, out[vb], 0, 0, 0);
-                        }
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int sb = 0; sb < 4; ++sb) {
-                    if (sb <= w) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-#pragma unroll
-                            for (int vb = 0; vb < VB; ++vb)
-                                out[vb] = __builtin_amdgcn_mfma_f32_16x16x4f32(zl[(16 * sb + 4 * g + i) * PZ + 16 * vb + c], sc[sb][i], out[vb], 0, 0, 0);
+                        for (int vb = 0; vb < VB; ++vb) mma32(out[vb], column(t.z[P], IC<RZ>{}, 16 * sb + 4 * g + i, vb), s);
                     }
                 }
             }
-            if (xrow < n) {
+            fetch_x(ch + 2, set);
+            int shift;
+            const auto o = os.next(ch, shift);
 #pragma unroll
-                for (int vb = 0; vb < VB; ++vb) store4((T*)(O + (ch * C + xrow) * sz) + 16 * vb + 4 * g, out[vb]);
-            }
+            for (int vb = 0; vb < VB; ++vb) put4<float>(o, oo - shift + 64 * vb, out[vb]);
+            if (ch + 1 < k.c1) st.template put<1 - P>(ch + 1);
+            st.template fetch<1 - P>(ch + 3);
+        };
+        for (int ch = k.c0; ch < k.c1; ch += 2) {
+            chunk(ch, IC<0>{});
+            if (ch + 1 < k.c1) chunk(ch + 1, IC<1>{});
         }
-        // the state behind the chunk
-        if (n < C) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) late[j] = late_token(j) < n ? dla_pow(ga, n - 1 - late_token(j)) : 0.f;
-        }
-        const int decays = n - (ch == 0 ? early : 0);
-        const float e = decays == C ? carry : decays == 0 ? 0.f : expm1f((float)decays * ga);
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-            for (int vb = 0; vb < VB; ++vb)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) S[kb][vb][i] = fmaf(S[kb][vb][i], e, S[kb][vb][i]);
-        if constexpr (ES == 2) {
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                bf16x8 hi[KB], lo[KB];
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb) {
-                    const bf16x8 y = Frag<bf16>::tr(yl, PY, 32 * kk, 16 * (w + 4 * kb), l);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float f = (float)y[j] * late[8 * kk + j];
-                        hi[kb][j] = (bf16)f;
-                        lo[kb][j] = (bf16)(f - (float)hi[kb][j]);
-                    }
-                }
-#pragma unroll
-                for (int vb = 0; vb < VB; ++vb) {
-                    const bf16x8 z = Frag<bf16>::tr(zl, PZ, 32 * kk, 16 * vb, l);
-#pragma unroll
-                    for (int kb = 0; kb < KB; ++kb) {
-                        Mfma<bf16>::mma(S[kb][vb], hi[kb], z);
-                        Mfma<bf16>::mma(S[kb][vb], lo[kb], z);
-                    }
-                }
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                float y[KB];
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb) y[kb] = yl[(4 * j + g) * PY + 16 * (w + 4 * kb) + c] * late[j];
-#pragma unroll
-                for (int vb = 0; vb < VB; ++vb) {
-                    const float z = zl[(4 * j + g) * PZ + 16 * vb + c];
-#pragma unroll
-                    for (int kb = 0; kb < KB; ++kb) mma32(S[kb][vb], y[kb], z);
-                }
-            }
-        }
-        if (ch + 1 < c1) {
-            stage(buf ^ 1);
-            if constexpr (!LOCAL) put_state(Sl[buf ^ 1]);
-        }
-    }
-
-    if constexpr (LOCAL) {
-        f32x4* dst = (f32x4*)(p.local + ((chain * (p.segs - 1) + sg) * slices + sl) * tsl) + tid;
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-            for (int vb = 0; vb < VB; ++vb) dst[(kb * VB + vb) * kDlaThreads] = S[kb][vb];
-    } else {
-        // the final state, by the segment of the last token; against time it is decayed once more (dS0 = a R_0)
-        if (ps.fin && (nch == 0 ? sg == 0 : c0 < nch && c1 == nch)) {
-            const float f = rev && L > 0 ? dla_pow(ga, 1) : 1.f;
-            each_state([&](f32x4& s, int i, long at) { ps.fin[at] = s[i] * f; });
-        }
-        // padding rows of the segment's part of the time axis
-        const long t0 = L > (long)c0 * C ? L : (long)c0 * C, t1 = sg + 1 < p.segs ? (long)(c0 + p.seg_chunks) * C : p.T;
-        char* out = (char*)ps.out + ((((long)b * p.T) * p.H + h) * V + sl * VS) * ES;
-        for (long x = tid; x < (t1 - t0) * ZR; x += kDlaThreads)
-            *(i32x4*)(out + (t0 + x / ZR) * p.H * V * ES + x % ZR * 16) = i32x4{0, 0, 0, 0};
+        k.pad(threadIdx.x, 256);
     }
 }
 
-DlaCut dla_cut(long B, long T, long H, int passes, int K, int V, bool f32) {
-    DlaCut c{32, 1, 1};
-    const long nch = (T + C - 1) / C, jobs = B * H * passes * (V / c.slice);
-    long segs = jobs > 0 ? 512 / jobs : 1;
-    segs = segs < nch / 16 ? segs : nch / 16;
+DlaCut dla_cut(long B, long T, long H, int passes, int V, bool f32) {
+    const long nch = (T + C - 1) / C, jobs = B * H * passes * (V / (f32 ? kDlaF32VS : kDlaVS)), least = 4;
+    long segs = jobs > 0 ? (f32 ? 256 : 512) / jobs : 1;
+    segs = segs < nch / least ? segs : nch / least;
     segs = segs < 1 ? 1 : segs;
+    DlaCut c{};
     c.seg_chunks = (int)((nch + segs - 1) / segs);
     c.seg_chunks = c.seg_chunks < 1 ? 1 : c.seg_chunks;
     c.segs = (int)((nch + c.seg_chunks - 1) / c.seg_chunks);
@@ -345,28 +703,22 @@ DlaCut dla_cut(long B, long T, long H, int passes, int K, int V, bool f32) {
     return c;
 }
 
-template <typename T, int K, int VS>
-static hipError_t launch_dla(int V, const DlaParams& p, hipStream_t s) {
-    const long per = (long)p.passes * (V / VS);
-    const long chains = (long)p.B * p.H;
-    if (p.segs > 1) {
-        const long n = chains * per * (p.segs - 1);
-        hipLaunchKernelGGL((gdr2_dla_kernel<T, K, VS, true>), dim3((unsigned)((n + 7) / 8 * 8)), dim3(kDlaThreads), 0, s, p, V, (int)n);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    const long n = chains * per * p.segs;
-    hipLaunchKernelGGL((gdr2_dla_kernel<T, K, VS, false>), dim3((unsigned)((n + 7) / 8 * 8)), dim3(kDlaThreads), 0, s, p, V, (int)n);
+template <int K, bool LOCAL>
+static hipError_t launch_dla(bool bf, int V, long n, const DlaParams& p, hipStream_t s) {
+    const dim3 grid((unsigned)((n + 7) / 8 * 8));
+    if (bf) hipLaunchKernelGGL((gdr2_dla_kernel<K, LOCAL>), grid, dim3(256), 0, s, p, V, (int)n);
+    else hipLaunchKernelGGL((gdr2_dla_f32_kernel<K, LOCAL>), grid, dim3(LOCAL ? 256 : 512), 0, s, p, V, (int)n);
     return hipGetLastError();
 }
 
-template <typename T>
-static hipError_t launch_dla(int K, int V, const DlaCut& c, const DlaParams& p, hipStream_t s) {
-    return K == 128 ? launch_dla<T, 128, 32>(V, p, s) : launch_dla<T, 64, 32>(V, p, s);
-}
-
-hipError_t dla_dispatch(int bf, int K, int V, const DlaCut& c, const DlaParams& p, hipStream_t s) {
-    return bf ? launch_dla<bf16>(K, V, c, p, s) : launch_dla<float>(K, V, c, p, s);
+hipError_t dla_dispatch(int bf, int K, int V, const DlaParams& p, hipStream_t s) {
+    const long per = (long)p.B * p.H * p.passes * (V / (bf ? kDlaVS : kDlaF32VS));  // workgroups of a segment
+    if (p.segs > 1) {
+        const long n = per * (p.segs - 1);
+        const hipError_t e = K == 128 ? launch_dla<128, true>(bf, V, n, p, s) : launch_dla<64, true>(bf, V, n, p, s);
+        if (e != hipSuccess) return e;
+    }
+    return K == 128 ? launch_dla<128, false>(bf, V, per * p.segs, p, s) : launch_dla<64, false>(bf, V, per * p.segs, p, s);
 }
 
 // One token: S <- a S + k v^T, o = S^T q.  A pure stream over the fp32 state, in registers, 16-byte accesses.

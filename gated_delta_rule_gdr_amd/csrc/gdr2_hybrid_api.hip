@@ -59,7 +59,7 @@ gdr2_status rms_fwd(gdr2::RmsKind kind, int64_t rows, int64_t D, gdr2_dtype dt, 
 // Afterwards B * H <= 2^20, B * T * H <= 2^30, and every launch fits: at most twelve workgroups per chain, or
 // (few chains) a few hundred.
 gdr2_status check_dla(int64_t B, int64_t T, int64_t H, int64_t dk, int64_t dv) {
-    if (B < 0 || T < 0 || H < 0 || dk < 0 || dv < 0 || T > ((int64_t)1 << 30)) return GDR2_E_SHAPE;
+    if (B < 0 || T < 0 || H < 0 || dk < 0 || dv < 0 || T > ((int64_t)1 << 30) || H > 32768) return GDR2_E_SHAPE;
     if (!dims_ok(dk) || !dims_ok(dv)) return GDR2_E_UNSUPPORTED;
     if (!prod_le(B, H, (int64_t)1 << 20) || !prod_le(B * H, (T + 63) / 64 + 1, ((int64_t)1 << 24) - 1)) return GDR2_E_SHAPE;
     return GDR2_OK;
@@ -70,7 +70,7 @@ struct DlaPlan {
     size_t total;
 };
 DlaPlan dla_plan(int64_t B, int64_t T, int64_t H, int passes, int K, int V, gdr2_dtype dt) {
-    DlaPlan d{gdr2::dla_cut(B, T, H, passes, K, V, dt == GDR2_F32), 0};
+    DlaPlan d{gdr2::dla_cut(B, T, H, passes, V, dt == GDR2_F32), 0};
     d.total = round_up((size_t)passes * B * H * (d.cut.segs - 1) * K * V * sizeof(float), 256);
     return d;
 }
@@ -169,8 +169,8 @@ gdr2_status gdr2_dla_fwd(int64_t B, int64_t T, int64_t H, int64_t dk, int64_t dv
     if (any_alias(outs, 3, ins, 6)) return GDR2_E_ALIAS;
     gdr2::DlaParams p = dla_params(d, B, T, H, log_decay, lengths, workspace);
     p.passes = 1;
-    p.pass[0] = {q, k, v, o, S0, S_T, 0, 0};
-    return status_of(gdr2::dla_dispatch(dt == GDR2_BF16, (int)dk, (int)dv, d.cut, p, (hipStream_t)stream));
+    p.pass[0] = {q, k, v, o, S0, S_T, 0, 0, 1};
+    return status_of(gdr2::dla_dispatch(dt == GDR2_BF16, (int)dk, (int)dv, p, (hipStream_t)stream));
 }
 
 // dq and dk contract over dv and leave dk columns, dv the other way round: three passes of one launch where
@@ -201,25 +201,26 @@ gdr2_status gdr2_dla_bwd(int64_t B, int64_t T, int64_t H, int64_t dk, int64_t dv
     const Range ins[] = {{q, n * dk}, {k, n * dk}, {v, n * dv}, {log_decay, (size_t)H * 4}, {S0, ns}, {lengths, (size_t)B * 4}, {dO, n * dv}, {dS_T, ns}};
     const Range outs[] = {{dq, n * dk}, {dk_, n * dk}, {dv_, n * dv}, {dS0, ns}, {workspace, need}};
     if (any_alias(outs, 5, ins, 8)) return GDR2_E_ALIAS;
-    const gdr2::DlaPass pq = {dO, v, k, dq, S0, nullptr, 0, 1}, pk = {v, dO, q, dk_, dS_T, nullptr, 1, 1}, pv = {k, q, dO, dv_, dS_T, dS0, 1, 0};
+    const gdr2::DlaPass pq = {dO, v, k, dq, S0, nullptr, 0, 1, 0}, pk = {v, dO, q, dk_, dS_T, nullptr, 1, 1, 0};
+    const gdr2::DlaPass pv = {k, q, dO, dv_, dS_T, dS0, 1, 0, 1};
     const bool bf = dt == GDR2_BF16;
     if (dk == dv) {
         const DlaPlan d = dla_plan(B, T, H, 3, (int)dk, (int)dv, dt);
         gdr2::DlaParams p = dla_params(d, B, T, H, log_decay, lengths, workspace);
         p.passes = 3;
         p.pass[0] = pq, p.pass[1] = pk, p.pass[2] = pv;
-        return status_of(gdr2::dla_dispatch(bf, (int)dk, (int)dv, d.cut, p, (hipStream_t)stream));
+        return status_of(gdr2::dla_dispatch(bf, (int)dk, (int)dv, p, (hipStream_t)stream));
     }
     const DlaPlan d2 = dla_plan(B, T, H, 2, (int)dv, (int)dk, dt), d1 = dla_plan(B, T, H, 1, (int)dk, (int)dv, dt);
     gdr2::DlaParams p = dla_params(d2, B, T, H, log_decay, lengths, workspace);
     p.passes = 2;
     p.pass[0] = pq, p.pass[1] = pk;
-    const hipError_t e = gdr2::dla_dispatch(bf, (int)dv, (int)dk, d2.cut, p, (hipStream_t)stream);
+    const hipError_t e = gdr2::dla_dispatch(bf, (int)dv, (int)dk, p, (hipStream_t)stream);
     if (e != hipSuccess) return GDR2_E_HIP;
     p = dla_params(d1, B, T, H, log_decay, lengths, workspace);
     p.passes = 1;
     p.pass[0] = pv;
-    return status_of(gdr2::dla_dispatch(bf, (int)dk, (int)dv, d1.cut, p, (hipStream_t)stream));
+    return status_of(gdr2::dla_dispatch(bf, (int)dk, (int)dv, p, (hipStream_t)stream));
 }
 
 gdr2_status gdr2_dla_step(int64_t N, int64_t H, int64_t dk, int64_t dv, gdr2_dtype dt, const void* q, const void* k,

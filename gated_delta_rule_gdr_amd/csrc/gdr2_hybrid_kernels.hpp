@@ -70,10 +70,10 @@ struct DlaPass {
     const float* init;      // the state before the first token, [B][H][K][V] or (flip) [B][H][V][K]; null = zero
     float* fin;             // the state behind the last one, likewise; null = not wanted
     int reverse, flip;
+    int state;              // whether the final state is a result of the operator, wanted or not
 };
 constexpr int kDlaChunk = 64;
 struct DlaCut {
-    int slice;              // columns of the state a workgroup carries: 32 or 64
     int segs, seg_chunks;   // segments of the sequence, and their chunks
 };
 struct DlaParams {
@@ -84,8 +84,8 @@ struct DlaParams {
     DlaPass pass[3];
     float* local;           // segs > 1: [passes][B][H][segs - 1][K * V] fp32, a segment's own state in the kernel's order
 };
-DlaCut dla_cut(long B, long T, long H, int passes, int K, int V, bool f32);
-hipError_t dla_dispatch(int dtype_bf16, int K, int V, const DlaCut& cut, const DlaParams& p, hipStream_t s);
+DlaCut dla_cut(long B, long T, long H, int passes, int V, bool f32);
+hipError_t dla_dispatch(int dtype_bf16, int K, int V, const DlaParams& p, hipStream_t s);
 struct DlaStepParams {
     long n;                 // N * H chains
     int H;

@@ -545,7 +545,7 @@ gdr2_status gdr2_rms_norm_q8_fwd(int64_t rows, int64_t D, gdr2_dtype dtype, int6
  * Linear attention with one fixed decay a_h = exp(log_decay_h) per head (no gradient flows to it):
  *     S_t = a S_{t-1} + k_t v_t^T,   o_t = S_t^T q_t   (the updated state is read, no query scale)
  * -- the mixer's update without its erase product, computed without the mixer's triangular solve.
- *   q, k, dq, dk    [B][T][H][dk]  dtype     dk, dv in {64, 128}; T <= 2^30, B H <= 2^20 and
+ *   q, k, dq, dk    [B][T][H][dk]  dtype     dk, dv in {64, 128}; T <= 2^30, H <= 32768, B H <= 2^20,
  *   v, o, dO, dv    [B][T][H][dv]  dtype     B H (ceil(T / 64) + 1) < 2^24 (else GDR2_E_SHAPE)
  *   log_decay       [H]            fp32      natural log, <= 0 (0: nothing is forgotten; -inf: all of it)
  *   S0, S_T, dS_T, dS0  [B][H][dk][dv] fp32 or NULL (inputs: zero; outputs: not wanted)
@@ -556,7 +556,7 @@ gdr2_status gdr2_rms_norm_q8_fwd(int64_t rows, int64_t D, gdr2_dtype dtype, int6
  * Both need a workspace of the size their query returns (0: none; the sequence is cut where there are few
  * chains).  gdr2_dla_step is one token for N sequences: S_out = a S_in + k v^T, o = S_out^T q, with S_in
  * [N][H][dk][dv] fp32 (NULL = zero; may equal S_out exactly); N H < 2^24.
- * Precision: states and every sum are fp32.  With GDR2_BF16 a decayed operand of the state's sums keeps 16
+ * Precision: states and every sum are fp32.  With GDR2_BF16 a decayed operand of the state's sums keeps 24
  * bits, and scores and the states as read are rounded to bf16 once each, as inputs of the matrix products.
  * A NaN or infinity stays in its sequence and head (products are formed over tiles: there it may also reach
  * rows before it).
