@@ -8,23 +8,33 @@
 // kept by the forward.  Chunks of 64 tokens: inside a chunk through the scores x_r . y_s, weighted a^(r - s);
 // from before it through the state, out_r += a^(r + 1) x_r S; then S <- a^64 S + sum_s a^(63 - s) y_s z_s^T.
 //
-// A workgroup carries 32 columns of one chain's state in fp32 registers (columns are independent), over the
+// A workgroup carries some columns of one chain's state in fp32 registers (columns are independent), over the
 // whole sequence or, where there are few chains, over one segment of it, whose entering state is put together from
 // the segments' own states (a first launch).  Scores are formed transposed (rows s, columns r), so that a lane's
-// weighted scores are operand values of the next product as they stand; the state is read from a bf16 copy in LDS
+// weighted scores are operand values of the next product as they stand; the state is read from a copy in LDS (bf16: rounded)
 // that each chunk writes for the next one.
 //
 // Rounding: S is carried in fp32, its decay as S + S (a^n - 1), so that slow decays lose nothing over long
-// sequences; the decayed operand of its sums is split into bf16 parts: three (24 bits) where the state is a result,
-// two where it is only read, as bf16.  Scores, and S as it is read, are
+// sequences.  For bf16 the decayed operand of its sums is split into bf16 parts: three (24 bits) where the state is a
+// result, two where it is only read, as bf16 (the third costs 3 % of a backward).  Scores, and S as it is read, are
 // rounded to bf16 once as inputs of their products, whose sums are fp32.  fp32 rounds nothing else.
+//
+// Measured (dk = dv = 128, bf16): B = 4, T = 4096, H = 16 forward 114 us (1.2 TB/s of its rows), backward 200 us (its
+// tensors, each once, would take 84 us; products 31 us); B = 1, T = 32768, H = 16 with its states 210 us.  The chain of steps
+// inside a chunk bounds it: scores wait for rows, products for scores, the next tiles for the products; a chunk takes 2.3 us
+// alone on a compute unit, two at once 3.5 us, with the matrix units a quarter busy, LDS a third, the caches' port a
+// third.  fp32 (B = 3, T = 777, H = 6, dk = 64, dv = 128): forward 29 us, backward 76 us, bound by the fp32 matrix rate: the
+// busiest of four SIMDs has 288 products of 32 cycles per chunk, 9200 of its 13000 cycles.
 #include "gdr2_common.hpp"
 #include "gdr2_hybrid_kernels.hpp"
 
 namespace gdr2 {
 
 constexpr int kDlaThreads = 256, C = kDlaChunk;
-constexpr int kDlaVS = 64, kDlaF32VS = 32;  // columns of a workgroup's state
+// Columns of a workgroup's state.  bf16: scores are formed again for every 64, and 64 is what registers hold with two
+// workgroups to a compute unit; with 32, forward and backward of B = 4, T = 4096, H = 16 took 361 us against 331, a prompt of
+// 32768 289 against 222.  fp32: 64 would leave no register for the rows ahead.
+constexpr int kDlaVS = 64, kDlaF32VS = 32;
 
 // a^n for whole n >= 0; a^0 = 1 also where a = 0
 __device__ __forceinline__ float dla_pow(float g, int n) { return n == 0 ? 1.f : expf((float)n * g); }
@@ -68,13 +78,6 @@ __device__ __forceinline__ float uniform(float x) {
     return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, x)));
 }
 
-// A wave-uniform value whose uses are not computed ahead of the loop they stand in (registers decide how many workgroups a
-// compute unit holds).
-__device__ __forceinline__ int fresh(int x) {
-    asm volatile("" : "+s"(x));
-    return x;
-}
-
 // The rows of one tensor, chunk by chunk.  A chunk is reached through a buffer descriptor that starts at its lowest row and
 // ends behind its highest, so the rows that a last chunk lacks lie outside of it (against time below it, at offsets that
 // wrap): they load as zeros and are not stored, without a branch.
@@ -100,7 +103,7 @@ struct DlaWork {
     static constexpr int RY = K * ES / 16, RZ = VS * ES / 16;    // pieces of a row
     const DlaParams& p;
     const DlaPass& ps;
-    int V, slices, sl, ip, sg, h, b;
+    int V, slices, ip, sl, sg, h, b;
     int L, nch, c0, c1;
     float ga;
     bool rev;
@@ -109,11 +112,11 @@ struct DlaWork {
 
     // Slices of a chain's columns lie next to each other, then passes, segments, heads, sequences: neighbours, which read
     // the same rows, run on one XCD.
-    __device__ __forceinline__ DlaWork(const DlaParams& q, int width, int item)
-        : p(q), ps(q.pass[item / (width / VS) % q.passes]), V(width), slices(width / VS) {
+    __device__ __forceinline__ DlaWork(const DlaParams& q, int item, int pass)
+        : p(q), ps(q.pass[pass]), V(ps.V), slices(V / VS), ip(pass) {
         const int segs = LOCAL ? p.segs - 1 : p.segs;
-        sl = item % slices, ip = item / slices % p.passes, sg = item / slices / p.passes % segs;
-        const int bh = item / slices / p.passes / segs;
+        sl = item % p.slots - ps.slot, sg = item / p.slots % segs;
+        const int bh = item / p.slots / segs;
         h = bh % p.H, b = bh / p.H;
         const int n = p.lengths ? p.lengths[b] : p.T;
         L = __builtin_amdgcn_readfirstlane(n < 0 ? 0 : n > p.T ? p.T : n);  // wave-uniform, for the descriptors
@@ -158,8 +161,8 @@ struct DlaWork {
 
 // Staging of y (16 bytes at a time, by NY threads) and z (four columns at a time, by NZ), z also as the decayed operand
 // z_s a^(63 - s) of the state's sums: for bf16 in parts of 8 bits each, three where the state is a result, two where it is only
-// read as bf16.  With two buffers (NB) set (ch - c0) % 2 of the
-// registers and of the tiles belongs to chunk ch.  Behind the last chunk nothing is loaded.
+// read as bf16.  With two buffers (NB) set (ch - c0) % 2 of the registers and of the tiles belongs to chunk ch.  Behind
+// the last chunk nothing is loaded.
 template <typename T, int K, int VS, bool LOCAL, int NY, int NZ, int NB>
 struct DlaStage {
     typedef DlaWork<T, K, VS, LOCAL> Work;
@@ -183,7 +186,7 @@ struct DlaStage {
     float late[ZU];  // a^(63 - s) of the staged rows
     bool exact;      // the third part too
     __device__ __forceinline__ DlaStage(const Work& work, Tiles& tiles, int ythread, int zthread)
-        : k(work), t(tiles), ys(work.rows_of_k(work.ps.y)), zs(work.rows_of_v(work.ps.z)), yt(ythread), zt(zthread), exact(LOCAL || (work.ps.state && work.final_here())) {
+        : k(work), t(tiles), ys(work.rows_of_k(work.ps.y)), zs(work.rows_of_v(work.ps.z)), yt(ythread), zt(zthread), exact(work.ps.state && (LOCAL || work.final_here())) {
 #pragma unroll
         for (int u = 0; u < YU; ++u) yo[u] = k.off((yt + u * NY) / RY, k.sx) + (yt + u * NY) % RY * 16;
 #pragma unroll
@@ -255,10 +258,17 @@ struct DlaStage {
     }
 };
 
-// The workgroup's place in the launch; -1: none.
-__device__ __forceinline__ int dla_item(int nwork) {
+// The workgroup's share of the launch goes to `body` with the length of its pass' rows: KM, or (KM = 0, dk and dv differ in
+// a backward) the pass' own.
+template <int KM, typename F>
+__device__ __forceinline__ void dla_share(const DlaParams& p, int nwork, F&& body) {
     const int per = gridDim.x / 8, item = blockIdx.x % 8 * per + blockIdx.x / 8;
-    return item < nwork ? item : -1;
+    if (item >= nwork) return;
+    int ip = 0;
+    while (ip + 1 < p.passes && item % p.slots >= p.pass[ip + 1].slot) ++ip;
+    if constexpr (KM) body(IC<KM>{}, item, ip);
+    else if (p.pass[ip].K == 128) body(IC<128>{}, item, ip);
+    else body(IC<64>{}, item, ip);
 }
 
 // ------------------------------------------------------------------ bf16
@@ -281,17 +291,20 @@ __device__ __forceinline__ void mma32x32(f32x16& c, const bf16x8& a, const bf16x
 __device__ __forceinline__ f32x16 zeros16() { return f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0}; }
 
 template <int K, bool LOCAL>
-__global__ __launch_bounds__(256, LOCAL ? 3 : 2) void gdr2_dla_kernel(DlaParams p, int V, int nwork) {
-    typedef DlaWork<bf16, K, kDlaVS, LOCAL> Work;
+struct DlaLds {
     typedef DlaStage<bf16, K, kDlaVS, LOCAL, LOCAL ? 256 : 128, 256, 1> Stage;
+    typename Stage::Tiles t;
+    i32x4 own[LOCAL ? 1 : 2][32 * 9];  // a reading wave's own: 64 channels of its rows, or its outputs
+};
+template <int K, bool LOCAL>
+__device__ __forceinline__ void dla_body(const DlaParams& p, i32x4* lds, int item, int ip) {
+    typedef DlaWork<bf16, K, kDlaVS, LOCAL> Work;
+    typedef typename DlaLds<K, LOCAL>::Stage Stage;
     constexpr int KK = K / 16, RY = Work::RY, RZ = Work::RZ, VB = kDlaVS / 32;
     // carrying waves, and the blocks of 32 x 32 of each: rows cw % NK + NK kb, columns cv + vb (times 32)
     constexpr int NW = LOCAL ? 4 : 2, NK = NW < K / 32 ? NW : K / 32, KB = K / 32 / NK, CB = VB * NK / NW;
-    __shared__ typename Stage::Tiles t;
-    __shared__ i32x4 Xl[LOCAL ? 1 : 2][32 * 9];  // a reading wave's own: 64 channels of its rows, or its outputs
-    const int item = dla_item(nwork);
-    if (item < 0) return;
-    const Work k(p, V, item);
+    auto& t = ((DlaLds<K, LOCAL>*)lds)->t;
+    const Work k(p, item, ip);
     if (LOCAL && k.c1 - k.c0 < p.seg_chunks) return;  // no later segment has a token: nobody reads this one's state
     const int l = lane_id(), w = __builtin_amdgcn_readfirstlane(wave_id()), n = l & 31, hf = l >> 5;
     Stage st(k, t, (int)threadIdx.x - (LOCAL ? 0 : 128), threadIdx.x);
@@ -385,7 +398,7 @@ __global__ __launch_bounds__(256, LOCAL ? 3 : 2) void gdr2_dla_kernel(DlaParams 
         // The wave's 32 rows arrive as whole lines (a lane's own pieces, as the products want them, would be 32 lines a
         // load), and outputs leave so; both turn round in the wave's own LDS.
         DlaStream xs = k.rows_of_k(k.ps.x), os = k.rows_of_v(k.ps.out);
-        i32x4* own = Xl[w];
+        i32x4* own = ((DlaLds<K, LOCAL>*)lds)->own[w];
         constexpr int XR = 8, XH = K / 64;  // pieces of a row and rounds: 64 channels at a time
         const int xrow = 32 * w + n;
         const int xo = k.off(32 * w + l / XR, k.sx) + l % XR * 16, oo = k.off(32 * w + l / RZ, k.sz) + l % RZ * 16;
@@ -506,20 +519,26 @@ __global__ __launch_bounds__(256, LOCAL ? 3 : 2) void gdr2_dla_kernel(DlaParams 
         k.pad(threadIdx.x, 128);
     }
 }
+template <int KM, bool LOCAL>
+__global__ __launch_bounds__(256, LOCAL ? 3 : 2) void gdr2_dla_kernel(DlaParams p, int nwork) {
+    __shared__ i32x4 lds[sizeof(DlaLds<KM ? KM : 128, LOCAL>) / 16];
+    dla_share<KM>(p, nwork, [&](auto k, int item, int ip) { dla_body<decltype(k)::value, LOCAL>(p, lds, item, ip); });
+}
 
 // ------------------------------------------------------------------ fp32
 // 16 x 16 products, of which this type's scores need eight times as many cycles: waves 0..3 read sixteen rows each,
 // waves 4..7 carry every fourth sixteen of the state's rows.
 template <int K, bool LOCAL>
-__global__ __launch_bounds__(LOCAL ? 256 : 512, 2) void gdr2_dla_f32_kernel(DlaParams p, int V, int nwork) {
-    constexpr int NT = LOCAL ? 256 : 512;
+struct DlaF32Stage : DlaStage<float, K, kDlaF32VS, LOCAL, LOCAL ? 256 : 512, LOCAL ? 256 : 512, 2> {
+    using DlaStage<float, K, kDlaF32VS, LOCAL, LOCAL ? 256 : 512, LOCAL ? 256 : 512, 2>::DlaStage;
+};
+template <int K, bool LOCAL>
+__device__ __forceinline__ void dla_f32_body(const DlaParams& p, i32x4* lds, int item, int ip) {
     typedef DlaWork<float, K, kDlaF32VS, LOCAL> Work;
-    typedef DlaStage<float, K, kDlaF32VS, LOCAL, NT, NT, 2> Stage;
+    typedef DlaF32Stage<K, LOCAL> Stage;
     constexpr int KP = K / 16, KB = K / 64, VB = kDlaF32VS / 16, RY = Work::RY, RZ = Work::RZ;
-    __shared__ typename Stage::Tiles t;
-    const int item = dla_item(nwork);
-    if (item < 0) return;
-    const Work k(p, V, item);
+    auto& t = *(typename Stage::Tiles*)lds;
+    const Work k(p, item, ip);
     if (LOCAL && k.c1 - k.c0 < p.seg_chunks) return;
     const int l = lane_id(), w = __builtin_amdgcn_readfirstlane(wave_id()), c = l & 15, g = l >> 4;
     // operand value of column 16 block + l % 16, contraction down the rows
@@ -689,9 +708,20 @@ __global__ __launch_bounds__(LOCAL ? 256 : 512, 2) void gdr2_dla_f32_kernel(DlaP
         k.pad(threadIdx.x, 256);
     }
 }
+template <int KM, bool LOCAL>
+__global__ __launch_bounds__(LOCAL ? 256 : 512, 2) void gdr2_dla_f32_kernel(DlaParams p, int nwork) {
+    __shared__ i32x4 lds[sizeof(typename DlaF32Stage<KM ? KM : 128, LOCAL>::Tiles) / 16];
+    dla_share<KM>(p, nwork, [&](auto k, int item, int ip) { dla_f32_body<decltype(k)::value, LOCAL>(p, lds, item, ip); });
+}
 
-DlaCut dla_cut(long B, long T, long H, int passes, int V, bool f32) {
-    const long nch = (T + C - 1) / C, jobs = B * H * passes * (V / (f32 ? kDlaF32VS : kDlaVS)), least = 4;
+// Segments of the sequence: as many as fill the device once (two workgroups of bf16 to a compute unit, one of fp32), none
+// below four chunks.  Measured for 128 / 256 / 384 / 512 / 768 / 1024 workgroups of bf16: B = 4, T = 4096, H = 16 forward
+// 152 / 140 / 130 / 123 / 131 / 137 us, B = 1, T = 32768, H = 16 467 / 254 / 245 / 225 / 245 / 252 (unsplit 1143); the
+// backward of the first, 384 workgroups in one segment, took 199 us, in two segments 242.  fp32, B = 3, T = 777, H = 6: at least
+// four chunks 29 us against 42 with at least sixteen (one segment); 512 instead of 256 workgroups made its backward 84 us
+// from 76.
+DlaCut dla_cut(long B, long T, long H, long slots, bool f32) {
+    const long nch = (T + C - 1) / C, jobs = B * H * slots, least = 4;
     long segs = jobs > 0 ? (f32 ? 256 : 512) / jobs : 1;
     segs = segs < nch / least ? segs : nch / least;
     segs = segs < 1 ? 1 : segs;
@@ -703,22 +733,29 @@ DlaCut dla_cut(long B, long T, long H, int passes, int V, bool f32) {
     return c;
 }
 
-template <int K, bool LOCAL>
-static hipError_t launch_dla(bool bf, int V, long n, const DlaParams& p, hipStream_t s) {
+template <int KM, bool LOCAL>
+static hipError_t launch_dla(bool bf, long n, const DlaParams& p, hipStream_t s) {
     const dim3 grid((unsigned)((n + 7) / 8 * 8));
-    if (bf) hipLaunchKernelGGL((gdr2_dla_kernel<K, LOCAL>), grid, dim3(256), 0, s, p, V, (int)n);
-    else hipLaunchKernelGGL((gdr2_dla_f32_kernel<K, LOCAL>), grid, dim3(LOCAL ? 256 : 512), 0, s, p, V, (int)n);
+    if (bf) hipLaunchKernelGGL((gdr2_dla_kernel<KM, LOCAL>), grid, dim3(256), 0, s, p, (int)n);
+    else hipLaunchKernelGGL((gdr2_dla_f32_kernel<KM, LOCAL>), grid, dim3(LOCAL ? 256 : 512), 0, s, p, (int)n);
     return hipGetLastError();
 }
+template <bool LOCAL>
+static hipError_t launch_dla_k(bool bf, long n, const DlaParams& p, hipStream_t s) {
+    for (int i = 1; i < p.passes; ++i)
+        if (p.pass[i].K != p.pass[0].K) return launch_dla<0, LOCAL>(bf, n, p, s);
+    return p.pass[0].K == 128 ? launch_dla<128, LOCAL>(bf, n, p, s) : launch_dla<64, LOCAL>(bf, n, p, s);
+}
 
-hipError_t dla_dispatch(int bf, int K, int V, const DlaParams& p, hipStream_t s) {
-    const long per = (long)p.B * p.H * p.passes * (V / (bf ? kDlaVS : kDlaF32VS));  // workgroups of a segment
+int dla_slots(int V, bool f32) { return V / (f32 ? kDlaF32VS : kDlaVS); }
+
+hipError_t dla_dispatch(int bf, const DlaParams& p, hipStream_t s) {
+    const long per = (long)p.B * p.H * p.slots;  // workgroups of a segment
     if (p.segs > 1) {
-        const long n = per * (p.segs - 1);
-        const hipError_t e = K == 128 ? launch_dla<128, true>(bf, V, n, p, s) : launch_dla<64, true>(bf, V, n, p, s);
+        const hipError_t e = launch_dla_k<true>(bf, per * (p.segs - 1), p, s);
         if (e != hipSuccess) return e;
     }
-    return K == 128 ? launch_dla<128, false>(bf, V, per * p.segs, p, s) : launch_dla<64, false>(bf, V, per * p.segs, p, s);
+    return launch_dla_k<false>(bf, per * p.segs, p, s);
 }
 
 // One token: S <- a S + k v^T, o = S^T q.  A pure stream over the fp32 state, in registers, 16-byte accesses.

@@ -56,31 +56,39 @@ gdr2_status rms_fwd(gdr2::RmsKind kind, int64_t rows, int64_t D, gdr2_dtype dt, 
 }
 
 // ------------------------------------------------------------------ linear attention with a decay per head
-// Afterwards B * H <= 2^20, B * T * H <= 2^30, and every launch fits: at most twelve workgroups per chain, or
-// (few chains) a few hundred.
+// Afterwards B * H <= 2^19, B * T * H <= 2^30, and every launch fits: at most twelve workgroups of 512 threads per
+// chain, or (few chains) at most 512 in all.
 gdr2_status check_dla(int64_t B, int64_t T, int64_t H, int64_t dk, int64_t dv) {
     if (B < 0 || T < 0 || H < 0 || dk < 0 || dv < 0 || T > ((int64_t)1 << 30) || H > 32768) return GDR2_E_SHAPE;
     if (!dims_ok(dk) || !dims_ok(dv)) return GDR2_E_UNSUPPORTED;
-    if (!prod_le(B, H, (int64_t)1 << 20) || !prod_le(B * H, (T + 63) / 64 + 1, ((int64_t)1 << 24) - 1)) return GDR2_E_SHAPE;
+    if (!prod_le(B, H, (int64_t)1 << 19) || !prod_le(B * H, (T + 63) / 64 + 1, ((int64_t)1 << 24) - 1)) return GDR2_E_SHAPE;
     return GDR2_OK;
 }
-// The passes of a call go into at most two launches: those with K = dv (dq, dk) and those with K = dk (o; dv).
+// The forward is one pass with dv columns; the backward's dq and dk have dk columns, dv has dv.
 struct DlaPlan {
     gdr2::DlaCut cut;
     size_t total;
 };
-DlaPlan dla_plan(int64_t B, int64_t T, int64_t H, int passes, int K, int V, gdr2_dtype dt) {
-    DlaPlan d{gdr2::dla_cut(B, T, H, passes, V, dt == GDR2_F32), 0};
-    d.total = round_up((size_t)passes * B * H * (d.cut.segs - 1) * K * V * sizeof(float), 256);
+DlaPlan dla_plan(bool bwd, int64_t B, int64_t T, int64_t H, int64_t dk, int64_t dv, gdr2_dtype dt) {
+    const bool f32 = dt == GDR2_F32;
+    const int slots = gdr2::dla_slots((int)dv, f32) + (bwd ? 2 * gdr2::dla_slots((int)dk, f32) : 0);
+    DlaPlan d{gdr2::dla_cut(B, T, H, slots, f32), 0};
+    d.total = round_up((size_t)(bwd ? 3 : 1) * B * H * (d.cut.segs - 1) * dk * dv * sizeof(float), 256);
     return d;
 }
-gdr2::DlaParams dla_params(const DlaPlan& d, int64_t B, int64_t T, int64_t H, const float* log_decay, const int32_t* lengths,
-                           void* ws) {
+template <size_t N>
+gdr2_status dla_run(const DlaPlan& d, int64_t B, int64_t T, int64_t H, gdr2_dtype dt, const gdr2::DlaPass (&pass)[N],
+                    const float* log_decay, const int32_t* lengths, void* ws, void* stream) {
     gdr2::DlaParams p{};
-    p.B = (int)B; p.T = (int)T; p.H = (int)H;
+    p.B = (int)B; p.T = (int)T; p.H = (int)H; p.passes = (int)N;
     p.segs = d.cut.segs; p.seg_chunks = d.cut.seg_chunks;
     p.log_decay = log_decay; p.lengths = lengths; p.local = (float*)ws;
-    return p;
+    for (size_t i = 0; i < N; ++i) {
+        p.pass[i] = pass[i];
+        p.pass[i].slot = p.slots;
+        p.slots += gdr2::dla_slots(pass[i].V, dt == GDR2_F32);
+    }
+    return status_of(gdr2::dla_dispatch(dt == GDR2_BF16, p, (hipStream_t)stream));
 }
 
 // ------------------------------------------------------------------ paged cache
@@ -149,7 +157,7 @@ gdr2_status gdr2_rms_norm_bwd(int64_t rows, int64_t D, gdr2_dtype dt, const void
 
 size_t gdr2_dla_fwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t dk, int64_t dv, gdr2_dtype dt) {
     if (!dtype_ok(dt) || check_dla(B, T, H, dk, dv) != GDR2_OK) return 0;
-    return dla_plan(B, T, H, 1, (int)dk, (int)dv, dt).total;
+    return dla_plan(false, B, T, H, dk, dv, dt).total;
 }
 
 gdr2_status gdr2_dla_fwd(int64_t B, int64_t T, int64_t H, int64_t dk, int64_t dv, gdr2_dtype dt, const void* q,
@@ -161,28 +169,20 @@ gdr2_status gdr2_dla_fwd(int64_t B, int64_t T, int64_t H, int64_t dk, int64_t dv
     if (B == 0 || H == 0) return GDR2_OK;
     if (!log_decay || (T > 0 && (!q || !k || !v || !o))) return GDR2_E_NULL;
     if (!all_aligned({q, k, v, S0, o, S_T, workspace}) || !aligned4(log_decay) || !aligned4(lengths)) return GDR2_E_ALIGN;
-    const DlaPlan d = dla_plan(B, T, H, 1, (int)dk, (int)dv, dt);
+    const DlaPlan d = dla_plan(false, B, T, H, dk, dv, dt);
     if (d.total > 0 && (!workspace || workspace_bytes < d.total)) return GDR2_E_WORKSPACE;
     const size_t n = (size_t)B * T * H * esize(dt), ns = (size_t)B * H * dk * dv * 4;
     const Range ins[] = {{q, n * dk}, {k, n * dk}, {v, n * dv}, {log_decay, (size_t)H * 4}, {S0, ns}, {lengths, (size_t)B * 4}};
     const Range outs[] = {{o, n * dv}, {S_T, ns}, {workspace, d.total}};
     if (any_alias(outs, 3, ins, 6)) return GDR2_E_ALIAS;
-    gdr2::DlaParams p = dla_params(d, B, T, H, log_decay, lengths, workspace);
-    p.passes = 1;
-    p.pass[0] = {q, k, v, o, S0, S_T, 0, 0, 1};
-    return status_of(gdr2::dla_dispatch(dt == GDR2_BF16, (int)dk, (int)dv, p, (hipStream_t)stream));
+    const int K = (int)dk, V = (int)dv;
+    const gdr2::DlaPass pass[] = {{K, V, q, k, v, o, S0, S_T, 0, 0, 1, 0}};
+    return dla_run(d, B, T, H, dt, pass, log_decay, lengths, workspace, stream);
 }
 
-// dq and dk contract over dv and leave dk columns, dv the other way round: three passes of one launch where
-// dk = dv, else two and one, which use the workspace in turn.
-static size_t dla_bwd_total(int64_t B, int64_t T, int64_t H, int64_t dk, int64_t dv, gdr2_dtype dt) {
-    if (dk == dv) return dla_plan(B, T, H, 3, (int)dk, (int)dv, dt).total;
-    const size_t a = dla_plan(B, T, H, 2, (int)dv, (int)dk, dt).total, b = dla_plan(B, T, H, 1, (int)dk, (int)dv, dt).total;
-    return a > b ? a : b;
-}
 size_t gdr2_dla_bwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t dk, int64_t dv, gdr2_dtype dt) {
     if (!dtype_ok(dt) || check_dla(B, T, H, dk, dv) != GDR2_OK) return 0;
-    return dla_bwd_total(B, T, H, dk, dv, dt);
+    return dla_plan(true, B, T, H, dk, dv, dt).total;
 }
 
 gdr2_status gdr2_dla_bwd(int64_t B, int64_t T, int64_t H, int64_t dk, int64_t dv, gdr2_dtype dt, const void* q,
@@ -195,32 +195,17 @@ gdr2_status gdr2_dla_bwd(int64_t B, int64_t T, int64_t H, int64_t dk, int64_t dv
     if (B == 0 || H == 0) return GDR2_OK;
     if (!log_decay || (T > 0 && (!q || !k || !v || !dO || !dq || !dk_ || !dv_))) return GDR2_E_NULL;
     if (!all_aligned({q, k, v, S0, dO, dS_T, dq, dk_, dv_, dS0, workspace}) || !aligned4(log_decay) || !aligned4(lengths)) return GDR2_E_ALIGN;
-    const size_t need = dla_bwd_total(B, T, H, dk, dv, dt);
-    if (need > 0 && (!workspace || workspace_bytes < need)) return GDR2_E_WORKSPACE;
+    const DlaPlan d = dla_plan(true, B, T, H, dk, dv, dt);
+    if (d.total > 0 && (!workspace || workspace_bytes < d.total)) return GDR2_E_WORKSPACE;
     const size_t n = (size_t)B * T * H * esize(dt), ns = (size_t)B * H * dk * dv * 4;
     const Range ins[] = {{q, n * dk}, {k, n * dk}, {v, n * dv}, {log_decay, (size_t)H * 4}, {S0, ns}, {lengths, (size_t)B * 4}, {dO, n * dv}, {dS_T, ns}};
-    const Range outs[] = {{dq, n * dk}, {dk_, n * dk}, {dv_, n * dv}, {dS0, ns}, {workspace, need}};
+    const Range outs[] = {{dq, n * dk}, {dk_, n * dk}, {dv_, n * dv}, {dS0, ns}, {workspace, d.total}};
     if (any_alias(outs, 5, ins, 8)) return GDR2_E_ALIAS;
-    const gdr2::DlaPass pq = {dO, v, k, dq, S0, nullptr, 0, 1, 0}, pk = {v, dO, q, dk_, dS_T, nullptr, 1, 1, 0};
-    const gdr2::DlaPass pv = {k, q, dO, dv_, dS_T, dS0, 1, 0, 1};
-    const bool bf = dt == GDR2_BF16;
-    if (dk == dv) {
-        const DlaPlan d = dla_plan(B, T, H, 3, (int)dk, (int)dv, dt);
-        gdr2::DlaParams p = dla_params(d, B, T, H, log_decay, lengths, workspace);
-        p.passes = 3;
-        p.pass[0] = pq, p.pass[1] = pk, p.pass[2] = pv;
-        return status_of(gdr2::dla_dispatch(bf, (int)dk, (int)dv, p, (hipStream_t)stream));
-    }
-    const DlaPlan d2 = dla_plan(B, T, H, 2, (int)dv, (int)dk, dt), d1 = dla_plan(B, T, H, 1, (int)dk, (int)dv, dt);
-    gdr2::DlaParams p = dla_params(d2, B, T, H, log_decay, lengths, workspace);
-    p.passes = 2;
-    p.pass[0] = pq, p.pass[1] = pk;
-    const hipError_t e = gdr2::dla_dispatch(bf, (int)dv, (int)dk, p, (hipStream_t)stream);
-    if (e != hipSuccess) return GDR2_E_HIP;
-    p = dla_params(d1, B, T, H, log_decay, lengths, workspace);
-    p.passes = 1;
-    p.pass[0] = pv;
-    return status_of(gdr2::dla_dispatch(bf, (int)dk, (int)dv, p, (hipStream_t)stream));
+    const int K = (int)dk, V = (int)dv;
+    const gdr2::DlaPass pass[] = {{V, K, dO, v, k, dq, S0, nullptr, 0, 1, 0, 0},
+                                  {V, K, v, dO, q, dk_, dS_T, nullptr, 1, 1, 0, 0},
+                                  {K, V, k, q, dO, dv_, dS_T, dS0, 1, 0, 1, 0}};
+    return dla_run(d, B, T, H, dt, pass, log_decay, lengths, workspace, stream);
 }
 
 gdr2_status gdr2_dla_step(int64_t N, int64_t H, int64_t dk, int64_t dv, gdr2_dtype dt, const void* q, const void* k,
@@ -265,7 +250,7 @@ gdr2_status gdr2_paged_cache_fill(int64_t B, int64_t T, int64_t Hkv, int64_t d, 
 size_t gdr2_paged_decode_workspace_bytes(int64_t N, int64_t H, int64_t Hkv, int64_t d, int64_t page, int64_t width) {
     if (check_paged_decode(N, H, Hkv, d, page, 0, width) != GDR2_OK) return 0;
     const int64_t groups = head_groups(H, Hkv);
-    const int splits = gdr2::paged_cut(N, Hkv, groups, page * width).splits;
+    const int splits = gdr2::paged_splits(N, Hkv, groups, page * width);
     return splits > 1 ? (size_t)N * Hkv * groups * splits * gdr2::kPagedHeads * (d + 4) * sizeof(float) : 0;
 }
 
@@ -286,11 +271,10 @@ gdr2_status gdr2_paged_decode_step(int64_t N, int64_t H, int64_t Hkv, int64_t d,
     const Range ins[] = {{q, nq}, {k, nk}, {v, nk}, {page_table, (size_t)N * width * 4}, {pos, (size_t)N * 4}};
     const Range outs[] = {{k_pages, nc}, {v_pages, nc}, {o, nq}, {workspace, need}};
     if (any_alias(outs, 4, ins, 5)) return GDR2_E_ALIAS;
-    const gdr2::PagedCut cut = gdr2::paged_cut(N, Hkv, head_groups(H, Hkv), page * width);
     gdr2::PagedDecodeParams p{};
     p.N = (int)N; p.H = (int)H; p.Hkv = (int)Hkv; p.d = (int)d; p.shift = shift_of(page); p.pages = (int)pages; p.width = (int)width;
     p.scale = scale; p.q = q; p.k = k; p.v = v; p.table = page_table; p.pos = pos; p.kp = k_pages; p.vp = v_pages; p.o = o;
-    p.splits = cut.splits; p.least = cut.least; p.part = (float*)workspace;
+    p.splits = gdr2::paged_splits(N, Hkv, head_groups(H, Hkv), page * width); p.part = (float*)workspace;
     return status_of(gdr2::paged_decode_dispatch(dt == GDR2_BF16, p, (hipStream_t)stream));
 }
 

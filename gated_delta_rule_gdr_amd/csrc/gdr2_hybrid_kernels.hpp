@@ -50,13 +50,9 @@ struct PagedDecodeParams {
     void *kp, *vp;
     void* o;                // [N][H][d]
     int splits;             // parts of the positions per (sequence, key/value head, head group)
-    int least;              // the fewest steps of a part (but for the last)
     float* part;            // splits > 1: [N][Hkv][groups][splits][16][d + 4] fp32 (a row, its maximum and sum)
 };
-struct PagedCut {
-    int splits, least;
-};
-PagedCut paged_cut(long N, long Hkv, long groups, long capacity);
+int paged_splits(long N, long Hkv, long groups, long capacity);
 hipError_t paged_decode_dispatch(int dtype_bf16, const PagedDecodeParams& p, hipStream_t s);
 
 // Linear attention with a fixed decay per head.  Every result of the forward and of the backward is one pass of
@@ -65,12 +61,14 @@ hipError_t paged_decode_dispatch(int dtype_bf16, const PagedDecodeParams& p, hip
 //     o: x, y, z = q, k, v     dq: dO, v, k     dk: v, dO, q (against time)     dv: k, q, dO (against time)
 // with the state, sums of a^.. y_s z_s^T, carried in fp32.
 struct DlaPass {
+    int K, V;
     const void *x, *y, *z;  // [B][T][H][K], [B][T][H][K], [B][T][H][V]
     void* out;              // [B][T][H][V]
     const float* init;      // the state before the first token, [B][H][K][V] or (flip) [B][H][V][K]; null = zero
     float* fin;             // the state behind the last one, likewise; null = not wanted
     int reverse, flip;
     int state;              // whether the final state is a result of the operator, wanted or not
+    int slot;               // slots of the passes before it
 };
 constexpr int kDlaChunk = 64;
 struct DlaCut {
@@ -78,14 +76,16 @@ struct DlaCut {
 };
 struct DlaParams {
     int B, T, H, passes;
+    int slots;              // workgroups of a segment of one chain, over the passes
     int segs, seg_chunks;
     const float* log_decay;
     const int* lengths;     // [B] or null
     DlaPass pass[3];
-    float* local;           // segs > 1: [passes][B][H][segs - 1][K * V] fp32, a segment's own state in the kernel's order
+    float* local;           // segs > 1: [passes][B][H][segs - 1][dk * dv] fp32, a segment's own state in the kernel's order
 };
-DlaCut dla_cut(long B, long T, long H, int passes, int V, bool f32);
-hipError_t dla_dispatch(int dtype_bf16, int K, int V, const DlaParams& p, hipStream_t s);
+int dla_slots(int V, bool f32);  // of a pass
+DlaCut dla_cut(long B, long T, long H, long slots, bool f32);
+hipError_t dla_dispatch(int dtype_bf16, const DlaParams& p, hipStream_t s);
 struct DlaStepParams {
     long n;                 // N * H chains
     int H;

@@ -10,6 +10,10 @@
 // Keys come as MFMA rows straight from memory (scores: positions in rows, heads in columns), so a lane's eight
 // probabilities are one head's, and the values it loads (its own positions, d / 16 channels) are the second
 // product's operand as they stand.  Waves, then parts, are joined by their running maxima.
+//
+// Measured (16 query heads over 4 of d = 128, bf16): 256 sequences of 1 to 4096 positions in pages of 16, 208 us with the
+// join, the rows at 4.6 TB/s of the 5.0 that a copy reaches; one sequence of 32768 positions in pages of 64, 15 us for the
+// rows (4.4 TB/s) and 6 for the join's launch.  The filling stores 4 prompts of up to 4096 tokens in 10 us, at a copy's rate.
 #include "gdr2_common.hpp"
 #include "gdr2_hybrid_kernels.hpp"
 
@@ -24,10 +28,9 @@ struct PagedSeq {
     __device__ __forceinline__ PagedSeq(const PagedDecodeParams& p, int sq) {
         const int pos = p.pos[sq], cap = p.width << p.shift;
         slots = pos < 0 ? 0 : (pos < cap ? pos : cap) + 1;
-        const int steps = (slots + kPagedStep - 1) / kPagedStep, even = (steps + p.splits - 1) / p.splits;
-        const int n = even > p.least ? even : p.least;
+        const int steps = (slots + kPagedStep - 1) / kPagedStep, n = (steps + p.splits - 1) / p.splits;
         per = n * kPagedStep;
-        live = (steps + n - 1) / n;
+        live = n > 0 ? (steps + n - 1) / n : 0;
     }
 };
 
@@ -238,11 +241,17 @@ __global__ __launch_bounds__(kPagedThreads) void gdr2_paged_join_kernel(PagedDec
     store4((T*)p.o + ((long)sq * p.H + head) * D + 4 * ln, o * (1.f / Z));
 }
 
-PagedCut paged_cut(long N, long Hkv, long groups, long capacity) {
+// Parts of the positions: as many as make 2048 workgroups with their sequences and heads, none below a step of 128.
+// That is more than the device holds at once: lengths differ, and so do the parts' ends.  Measured for 256 / 512 / 1024 /
+// 2048 / 4096 workgroups (16 query heads over 4 of d = 128, bf16): 256 sequences of 1 to 4096 positions 219 / 219 / 219 /
+// 208 / 206 us, one of 32768 18 / 18 / 21 / 21 / 21, 32 of 1 to 4096 40 / 31 / 33 / 32 / 40; and 13 of 1 to 2777, fp32,
+// 12 over 4 heads of d = 64, 20 / 19 / 17 / 14.5 / 15.  Up to three steps stay one part, since the launch that joins parts
+// costs as much as two steps: 64 sequences of 300 positions 7.7 us in one part each, 10.3 in three; one of 500 (four steps)
+// 7.5 us in four parts, 9.1 in two.
+int paged_splits(long N, long Hkv, long groups, long capacity) {
     const long jobs = N * Hkv * groups, steps = (capacity + kPagedStep) / kPagedStep;  // the new token included
-    long want = jobs > 0 ? 2048 / jobs : 1;
-    const long s = want < steps ? want : steps;
-    return PagedCut{(int)(s < 1 ? 1 : s), 1};
+    if (steps <= 3 || jobs < 1 || jobs > 1024) return 1;
+    return (int)(2048 / jobs < steps ? 2048 / jobs : steps);
 }
 
 template <typename T, int D>

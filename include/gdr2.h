@@ -545,7 +545,7 @@ gdr2_status gdr2_rms_norm_q8_fwd(int64_t rows, int64_t D, gdr2_dtype dtype, int6
  * Linear attention with one fixed decay a_h = exp(log_decay_h) per head (no gradient flows to it):
  *     S_t = a S_{t-1} + k_t v_t^T,   o_t = S_t^T q_t   (the updated state is read, no query scale)
  * -- the mixer's update without its erase product, computed without the mixer's triangular solve.
- *   q, k, dq, dk    [B][T][H][dk]  dtype     dk, dv in {64, 128}; T <= 2^30, H <= 32768, B H <= 2^20,
+ *   q, k, dq, dk    [B][T][H][dk]  dtype     dk, dv in {64, 128}; T <= 2^30, H <= 32768, B H <= 2^19,
  *   v, o, dO, dv    [B][T][H][dv]  dtype     B H (ceil(T / 64) + 1) < 2^24 (else GDR2_E_SHAPE)
  *   log_decay       [H]            fp32      natural log, <= 0 (0: nothing is forgotten; -inf: all of it)
  *   S0, S_T, dS_T, dS0  [B][H][dk][dv] fp32 or NULL (inputs: zero; outputs: not wanted)
@@ -557,7 +557,8 @@ gdr2_status gdr2_rms_norm_q8_fwd(int64_t rows, int64_t D, gdr2_dtype dtype, int6
  * chains).  gdr2_dla_step is one token for N sequences: S_out = a S_in + k v^T, o = S_out^T q, with S_in
  * [N][H][dk][dv] fp32 (NULL = zero; may equal S_out exactly); N H < 2^24.
  * Precision: states and every sum are fp32.  With GDR2_BF16 a decayed operand of the state's sums keeps 24
- * bits, and scores and the states as read are rounded to bf16 once each, as inputs of the matrix products.
+ * bits in S_T and dS0 and 16 in states that are only read; scores and the states as read are rounded to bf16 once
+ * each, as inputs of the matrix products.
  * A NaN or infinity stays in its sequence and head (products are formed over tiles: there it may also reach
  * rows before it).
  */
@@ -579,11 +580,13 @@ gdr2_status gdr2_dla_step(int64_t N, int64_t H, int64_t dk, int64_t dv, gdr2_dty
                           const float* S_in, float* S_out, void* o, void* stream);
 
 /*
- * A key/value cache of pages: k_pages and v_pages [pages][page][Hkv][d] in dtype, page a power of two,
- * (else GDR2_E_VALUE), pages * page < 2^31; page_table [N][width] int32, width * page <= 2^30, N * width <= 2^40.  Position p of a sequence n is row
- * p % page of page page_table[n][p / page].  A position behind the table, or whose entry lies outside of
- * [0, pages), has no row: nothing is stored at it and attention does not see it.  Sequences may share pages
- * that no call writes to; rows that one call writes for two tokens hold either token's values.
+ * A key/value cache of pages: k_pages and v_pages [pages][page][Hkv][d] in dtype, page a power of two (else
+ * GDR2_E_VALUE), pages * page < 2^31; page_table [N][width] int32, width * page <= 2^30, N * width <= 2^40.
+ * Position p of a sequence n is row p % page of page page_table[n][p / page].  A position behind the table, or
+ * whose entry lies outside of [0, pages), has no row: nothing is stored at it and attention does not see it.
+ * Sequences may share pages (a common prefix) whose rows no call writes.  A row that a call writes must be one
+ * position of one sequence: where two tokens are written to one, each 16 bytes of it are either token's, and a step that
+ * also reads the row it writes as another position sees either its old or its new values.
  *
  * gdr2_paged_cache_fill stores, from a prefill's k and v ([B][T][Hkv][d]), token t < lengths[b] of sequence b
  * at position start[b] + t (lengths NULL: T tokens, values clamped to [0, T]; start NULL: 0; a negative position
