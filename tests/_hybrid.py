@@ -7,7 +7,8 @@ n g, at most |n g| <= 64 |g| inside a chunk; weights that small are bounded by n
 state's power is formed from one argument), a sum over 64 tokens, and one rounding of the state per later
 chunk (at most ceil(T / 64), and as many for segments): c32 = (2 K + 128 + 4 ceil(T / 64) + 64) u32, times `all`.
 With bf16 the scores of a chunk and the state as it is read are each rounded once (u16: `score`, `read`), the
-state's decayed operand keeps 16 bits (2^-16, times `all`; `state` for a final state), and outputs are rounded once.
+state's decayed operand keeps 16 bits, cut (2^-15, times `all`; 24 bits, 2^-23 times `state`, for a final state),
+and outputs are rounded once.
 
 Normwise: roundings of a half step are at most u / sqrt(3) of the value in the mean square for each of three
 roundings whose errors add in squares where terms have either sign: below u16 = sqrt(3) u16 / sqrt(3); 2 u16 leaves room for
@@ -25,13 +26,13 @@ def dla_c32(K, T):
 
 
 def dla_bounds(r, ref, dtype, K, T):
-    c = dla_c32(K, T) + (2.0 ** -16 if dtype == "bf16" else 0.0)
+    c = dla_c32(K, T) + (2.0 ** -15 if dtype == "bf16" else 0.0)
     low = U16 * (1 + 2.0 ** -7) * (r["score"] + r["read"]) if dtype == "bf16" else 0.0
     return low + c * r["all"] + U[dtype] * np.abs(ref) * (1 + 2.0 ** -7) + 1e-30
 
 
 def dla_state_bounds(r, dtype, K, T):
-    return (dla_c32(K, T) + (2.0 ** -16 if dtype == "bf16" else 0.0)) * r["state"] + 1e-30
+    return (dla_c32(K, T) + (2.0 ** -23 if dtype == "bf16" else 0.0)) * r["state"] + 1e-30
 
 
 def norm_close(name, got, ref, dtype, K, T):
