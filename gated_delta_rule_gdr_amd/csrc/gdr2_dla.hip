@@ -17,7 +17,8 @@
 // Rounding: S is carried in fp32, its decay as S + S (a^n - 1), so that slow decays lose nothing over long
 // sequences.  For bf16 the decayed operand of its sums is split into bf16 parts: three (24 bits) where the state is a
 // result, two where it is only read, as bf16 (the third costs 3 % of a backward).  Scores, and S as it is read, are
-// rounded to bf16 once as inputs of their products, whose sums are fp32.  fp32 rounds nothing else.
+// rounded to bf16 once as inputs of their products (in short sequences: split in two), whose sums are fp32.  fp32 rounds
+// nothing else.
 //
 // Measured (dk = dv = 128, bf16): B = 4, T = 4096, H = 16 forward 114 us (1.2 TB/s of its rows), backward 200 us (its
 // tensors, each once, would take 84 us; products 31 us); B = 1, T = 32768, H = 16 with its states 210 us.  The chain of steps
@@ -35,6 +36,11 @@ constexpr int kDlaThreads = 256, C = kDlaChunk;
 // workgroups to a compute unit; with 32, forward and backward of B = 4, T = 4096, H = 16 took 361 us against 331, a prompt of
 // 32768 289 against 222.  fp32: 64 would leave no register for the rows ahead.
 constexpr int kDlaVS = 64, kDlaF32VS = 32;
+// Up to this length bf16 keeps 16 bits of the scores and of the state as it is read (two products each): sums that short do
+// not average roundings out.  Normwise error over that of the exact result rounded once, 1 to 64 tokens of a few
+// heads: 1.0 against up to 1.96; from 129 tokens on it is 1.41 to 1.44 with one rounding each.  It costs 64 prompts of 128 tokens
+// (H = 16, dk = dv = 128) 66 us for 59, their backward 144 for 123; fewer chains less than a microsecond.
+constexpr int kDlaFine = 128;
 
 // a^n for whole n >= 0; a^0 = 1 also where a = 0
 __device__ __forceinline__ float dla_pow(float g, int n) { return n == 0 ? 1.f : expf((float)n * g); }
@@ -296,7 +302,9 @@ struct DlaLds {
     typename Stage::Tiles t;
     i32x4 own[LOCAL ? 1 : 2][32 * 9];  // a reading wave's own: 64 channels of its rows, or its outputs
 };
-template <int K, bool LOCAL>
+// FINE: scores and the state as it is read in two parts each; the state's second part takes the first one's place in LDS
+// between two more barriers.
+template <int K, bool LOCAL, bool FINE>
 __device__ __forceinline__ void dla_body(const DlaParams& p, i32x4* lds, int item, int ip) {
     typedef DlaWork<bf16, K, kDlaVS, LOCAL> Work;
     typedef typename DlaLds<K, LOCAL>::Stage Stage;
@@ -347,6 +355,17 @@ __device__ __forceinline__ void dla_body(const DlaParams& p, i32x4* lds, int ite
                         store4((bf16*)(t.s[0] + (32 * vb + n) * Stage::RS + 4 * kb + i) + 4 * hf, f32x4{s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]});
                 });
         };
+        auto put_rest = [&]() {  // what rounding left of it
+            each_block([&](const f32x16& s, int kb, int vb) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    f32x4 r;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) r[e] = s[4 * i + e] - (float)(bf16)s[4 * i + e];
+                    store4((bf16*)(t.s[0] + (32 * vb + n) * Stage::RS + 4 * kb + i) + 4 * hf, r);
+                }
+            });
+        };
         const float whole = expm1f((float)C * k.ga);
         if (k.c0 < k.c1) {
             st.template fetch<0>(k.c0);
@@ -356,6 +375,11 @@ __device__ __forceinline__ void dla_body(const DlaParams& p, i32x4* lds, int ite
         }
         for (int ch = k.c0; ch < k.c1; ++ch) {
             lds_barrier();
+            if constexpr (FINE) {
+                lds_barrier();
+                put_rest();
+                lds_barrier();
+            }
             const float e = k.decay(ch, whole);
             each_block([&](f32x16& s, int, int) {
 #pragma unroll
@@ -478,6 +502,15 @@ __device__ __forceinline__ void dla_body(const DlaParams& p, i32x4* lds, int ite
                 for (int vb = 0; vb < VB; ++vb)
                     mma32x32(out[vb], __builtin_bit_cast(bf16x8, t.s[0][(32 * vb + n) * Stage::RS + 2 * kk + hf]), x);
             }
+            if constexpr (FINE) {
+                lds_barrier();
+                lds_barrier();
+#pragma unroll
+                for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+                    for (int vb = 0; vb < VB; ++vb)
+                        mma32x32(out[vb], __builtin_bit_cast(bf16x8, t.s[0][(32 * vb + n) * Stage::RS + 2 * kk + hf]), __builtin_bit_cast(bf16x8, xr[kk]));
+            }
             const float f = ch == 0 ? before0 : before;
 #pragma unroll
             for (int vb = 0; vb < VB; ++vb)
@@ -488,15 +521,21 @@ __device__ __forceinline__ void dla_body(const DlaParams& p, i32x4* lds, int ite
                 constexpr bool SELF = decltype(inside)::value;
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk) {
-                    bf16x8 pr;
+                    bf16x8 pr, rest;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const int j = 2 * kk + e / 4, i = e % 4;
                         const float wt = SELF ? j == on ? diag[i] : self[j] * fall[i] : prev[j] * fall[i];
-                        pr[e] = (bf16)(score[8 * kk + e] * wt);
+                        const float x = score[8 * kk + e] * wt;
+                        pr[e] = (bf16)x;
+                        if constexpr (FINE) rest[e] = (bf16)(x - (float)pr[e]);
                     }
 #pragma unroll
-                    for (int vb = 0; vb < VB; ++vb) mma32x32(out[vb], columns32<RZ>(t.z[0], r0 + 16 * kk, 4 * vb, l), pr);
+                    for (int vb = 0; vb < VB; ++vb) {
+                        const bf16x8 z = columns32<RZ>(t.z[0], r0 + 16 * kk, 4 * vb, l);
+                        mma32x32(out[vb], z, pr);
+                        if constexpr (FINE) mma32x32(out[vb], z, rest);
+                    }
                 }
             };
             add(sc, 32 * w, IC<1>{});
@@ -519,10 +558,10 @@ __device__ __forceinline__ void dla_body(const DlaParams& p, i32x4* lds, int ite
         k.pad(threadIdx.x, 128);
     }
 }
-template <int KM, bool LOCAL>
+template <int KM, bool LOCAL, bool FINE>
 __global__ __launch_bounds__(256, LOCAL ? 3 : 2) void gdr2_dla_kernel(DlaParams p, int nwork) {
     __shared__ i32x4 lds[sizeof(DlaLds<KM ? KM : 128, LOCAL>) / 16];
-    dla_share<KM>(p, nwork, [&](auto k, int item, int ip) { dla_body<decltype(k)::value, LOCAL>(p, lds, item, ip); });
+    dla_share<KM>(p, nwork, [&](auto k, int item, int ip) { dla_body<decltype(k)::value, LOCAL, FINE>(p, lds, item, ip); });
 }
 
 // ------------------------------------------------------------------ fp32
@@ -736,7 +775,8 @@ DlaCut dla_cut(long B, long T, long H, long slots, bool f32) {
 template <int KM, bool LOCAL>
 static hipError_t launch_dla(bool bf, long n, const DlaParams& p, hipStream_t s) {
     const dim3 grid((unsigned)((n + 7) / 8 * 8));
-    if (bf) hipLaunchKernelGGL((gdr2_dla_kernel<KM, LOCAL>), grid, dim3(256), 0, s, p, (int)n);
+    if (bf && !LOCAL && p.T <= kDlaFine) hipLaunchKernelGGL((gdr2_dla_kernel<KM, false, true>), grid, dim3(256), 0, s, p, (int)n);
+    else if (bf) hipLaunchKernelGGL((gdr2_dla_kernel<KM, LOCAL, false>), grid, dim3(256), 0, s, p, (int)n);
     else hipLaunchKernelGGL((gdr2_dla_f32_kernel<KM, LOCAL>), grid, dim3(LOCAL ? 256 : 512), 0, s, p, (int)n);
     return hipGetLastError();
 }

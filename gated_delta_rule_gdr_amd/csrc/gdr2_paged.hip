@@ -137,13 +137,22 @@ __global__ __launch_bounds__(kPagedThreads, 2) void gdr2_paged_decode_kernel(Pag
                 s[b][r] = __builtin_amdgcn_exp2f(s[b][r] - m);
                 z += s[b][r];
             }
-        // probabilities rounded to bf16 for the bf16 product (its inputs' precision), sums in fp32
+        // bf16: probabilities in two parts, 16 bits (with one, a few positions do not average its roundings out; the second
+        // product is free beside the rows' arrival), sums in fp32
+        bf16x8 w, rest;
+        if constexpr (ES == 2) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                w[e] = (bf16)s[e / 4][e % 4];
+                rest[e] = (bf16)(s[e / 4][e % 4] - (float)w[e]);
+            }
+        }
 #pragma unroll
         for (int i = 0; i < DPL; ++i) {
             if constexpr (ES == 2) {
                 const bf16x8 a = {vf[0][0][i], vf[0][1][i], vf[0][2][i], vf[0][3][i], vf[1][0][i], vf[1][1][i], vf[1][2][i], vf[1][3][i]};
-                const bf16x8 w = {(bf16)s[0][0], (bf16)s[0][1], (bf16)s[0][2], (bf16)s[0][3], (bf16)s[1][0], (bf16)s[1][1], (bf16)s[1][2], (bf16)s[1][3]};
                 acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, w, acc[i], 0, 0, 0);
+                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, rest, acc[i], 0, 0, 0);
             } else {
 #pragma unroll
                 for (int b = 0; b < 2; ++b)

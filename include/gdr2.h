@@ -558,7 +558,7 @@ gdr2_status gdr2_rms_norm_q8_fwd(int64_t rows, int64_t D, gdr2_dtype dtype, int6
  * [N][H][dk][dv] fp32 (NULL = zero; may equal S_out exactly); N H < 2^24.
  * Precision: states and every sum are fp32.  With GDR2_BF16 a decayed operand of the state's sums keeps 24
  * bits in S_T and dS0 and 16 in states that are only read; scores and the states as read are rounded to bf16 once
- * each, as inputs of the matrix products.
+ * each, as inputs of the matrix products, but for T <= 128, where they keep 16 bits.
  * A NaN or infinity stays in its sequence and head (products are formed over tiles: there it may also reach
  * rows before it).
  */
@@ -597,7 +597,7 @@ gdr2_status gdr2_dla_step(int64_t N, int64_t H, int64_t dk, int64_t dv, gdr2_dty
  * token: o is zero, nothing is stored.
  *   H a multiple of Hkv, H <= 32768, d in {64, 128}, N * H <= 2^30, B * T * Hkv <= 2^32; scale > 0, finite
  *   workspace   gdr2_paged_decode_workspace_bytes() bytes (0: none needed)
- * Precision as in gdr2_swa_decode_step: fp32 throughout, but for bf16 probabilities as inputs of their product.
+ * Precision: fp32 throughout; with GDR2_BF16 the probabilities keep 16 bits as inputs of their product.
  */
 gdr2_status gdr2_paged_cache_fill(int64_t B, int64_t T, int64_t Hkv, int64_t d, gdr2_dtype dtype,
                                   int64_t page, int64_t pages, int64_t width, const void* k,

@@ -7,7 +7,7 @@ import torch
 import gated_delta_rule_gdr_amd as g2
 from oracle import hybrid
 from tests._block import DT, U, U32, f64, randn, swa_bounds, within
-from tests._hybrid import dla_bounds, dla_state_bounds, norm_close
+from tests._hybrid import dla_bounds, dla_c32, dla_state_bounds, norm_close
 from tests._util import announce
 
 pytestmark = pytest.mark.gpu
@@ -191,6 +191,30 @@ def test_dla_segments(dtype, dk, dv):
     assert g2.dla_fwd_workspace_bytes(3, 2500, 1, dk, dv, DT[dtype]) > 0
     _dla_check(3, 2500, 1, dk, dv, dtype, [2500, 1300, 1024], seed=2, garbage=float("inf"))
     _dla_check(1, 2048, 2, dk, dv, dtype, None, seed=6)
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 64), (64, 128), (128, 128)])
+@pytest.mark.parametrize("T", [1, 2, 3, 7, 40, 65, 128])
+def test_dla_short_sequences_round_once(T, dk, dv):
+    """bf16, few tokens: what the products take keeps 16 bits, 2^-15 of the terms at most for each of three operands (the
+    scores, the state as read, the state's decayed operand), so the error is that of the result's own rounding, u16, and
+    3 2^-15 `all`."""
+    announce(f"dla short T={T} dk={dk} dv={dv}")
+    x = _dla_inputs(1, T, 1, dk, dv, "bf16", 3 * T)
+    x["g"] = torch.tensor([-0.05])
+    d = {n: t.to(DEV) for n, t in x.items()}
+    f = {n: f64(t) for n, t in x.items()}
+    o, _ = g2.gdr2_dla_fwd(d["q"], d["k"], d["v"], d["g"], d["S0"])
+    gr = g2.gdr2_dla_bwd(d["q"], d["k"], d["v"], d["g"], d["dO"], d["S0"], d["dS_T"])
+    ro, _ = hybrid.dla_forward(f["q"], f["k"], f["v"], f["g"], f["S0"])
+    rg = hybrid.dla_backward(f["q"], f["k"], f["v"], f["g"], f["dO"], f["S0"], f["dS_T"])
+    flip = lambda t: np.swapaxes(t, -1, -2)  # noqa: E731
+    for name, got, ref, (a, b, c), init, rev in (
+            ("o", o, ro, ("q", "k", "v"), f["S0"], False), ("dq", gr["dq"], rg["dq"], ("dO", "v", "k"), flip(f["S0"]), False),
+            ("dk", gr["dk"], rg["dk"], ("v", "dO", "q"), flip(f["dS_T"]), True), ("dv", gr["dv"], rg["dv"], ("k", "q", "dO"), f["dS_T"], True)):
+        r = hybrid.dla_sizes(f[a], f[b], f[c], f["g"], init, None, rev)
+        low = (3 * 2.0 ** -15 + dla_c32(f[a].shape[-1], T)) * r["all"]
+        within(name, got, ref, low + U["bf16"] * (1 + 2.0 ** -7) * np.abs(ref) + 1e-30)
 
 
 def test_dla_defaults_empty_and_deterministic():
@@ -382,3 +406,19 @@ def test_paged_decode_large_scores_and_shared_prefix():
     r = hybrid.paged_decode(f64(q), f64(k), f64(v), f64(kp), f64(vp), table.tolist(), [32, 40], d ** -0.5)
     within("o", o, r["o"], swa_bounds(dict(r, lse=np.zeros(())), "bf16", d, 41)["o"])
     assert np.array_equal(f64(kpd), r["k_pages"])
+
+
+@pytest.mark.parametrize("n", [1, 2, 3, 6, 20, 33])
+def test_paged_decode_few_positions_round_once(n):
+    """bf16: probabilities keep 16 bits (2^-16 of each, half a step), so the error is that of the result's own rounding and
+    the fp32 bounds of the sums."""
+    gen = torch.Generator().manual_seed(n)
+    H, Hkv, d, page = 4, 2, 64, 16
+    kp, vp = randn(gen, (3, page, Hkv, d), "bf16"), randn(gen, (3, page, Hkv, d), "bf16")
+    q, k, v = randn(gen, (1, H, d), "bf16"), randn(gen, (1, Hkv, d), "bf16"), randn(gen, (1, Hkv, d), "bf16")
+    table = torch.tensor([[2, 0, 1]], dtype=I32)
+    kpd, vpd, qd, kd, vd, td = dev(kp, vp, q, k, v, table)
+    o = g2.gdr2_paged_decode_step(qd, kd, vd, kpd, vpd, td, i32([n - 1]))
+    r = hybrid.paged_decode(f64(q), f64(k), f64(v), f64(kp), f64(vp), table.tolist(), [n - 1], d ** -0.5)
+    fine = swa_bounds(dict(r, lse=np.zeros(())), "f32", d, n)["o"] + 2.0 ** -16 * r["o_abs"]
+    within("o", o, r["o"], fine + U["bf16"] * (1 + 2.0 ** -7) * np.abs(r["o"]))
