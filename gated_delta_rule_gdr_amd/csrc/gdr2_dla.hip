@@ -53,11 +53,10 @@ __device__ __forceinline__ int tile_at(int row, int piece) {
     if constexpr (sizeof(T) == 2) {
         const int b = ((row >> 2) ^ (row >> 3)) & 1, t = row >> 1;
         if constexpr (R == 16) return row * R + (piece ^ ((row & 3) << 2 | b << 1 | ((row >> 2) & 1)));
-        if constexpr (R == 8) return row * R + (piece ^ ((t & 1) << 2 | b << 1 | ((t >> 1) & 1)));
-        return row * R + piece;  // four rows of 64 bytes are all banks
+        else return row * R + (piece ^ ((t & 1) << 2 | b << 1 | ((t >> 1) & 1)));
     } else {
         if constexpr (R >= 16) return row * R + (piece ^ (row & 15));
-        return (row * R + piece) ^ (((row >> 2) & 1) << 3 | ((row >> 3) & 1) << 2);
+        else return (row * R + piece) ^ (((row >> 2) & 1) << 3 | ((row >> 3) & 1) << 2);
     }
 }
 
@@ -74,11 +73,6 @@ template <typename T>
 __device__ __forceinline__ typename Raw4<T>::t load4(__amdgpu_buffer_rsrc_t t, int offset) {
     if constexpr (sizeof(T) == 2) return __builtin_bit_cast(bf16x4, __builtin_amdgcn_raw_buffer_load_b64(t, offset, 0, 0));
     else return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(t, offset, 0, 0));
-}
-template <typename T>
-__device__ __forceinline__ void put4(__amdgpu_buffer_rsrc_t t, int offset, const f32x4& v) {
-    if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, Raw4<bf16>::narrow(v)), t, offset, 0, 0);
-    else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), t, offset, 0, 0);
 }
 __device__ __forceinline__ float uniform(float x) {
     return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, x)));
@@ -568,9 +562,7 @@ __global__ __launch_bounds__(256, LOCAL ? 3 : 2) void gdr2_dla_kernel(DlaParams 
 // 16 x 16 products, of which this type's scores need eight times as many cycles: waves 0..3 read sixteen rows each,
 // waves 4..7 carry every fourth sixteen of the state's rows.
 template <int K, bool LOCAL>
-struct DlaF32Stage : DlaStage<float, K, kDlaF32VS, LOCAL, LOCAL ? 256 : 512, LOCAL ? 256 : 512, 2> {
-    using DlaStage<float, K, kDlaF32VS, LOCAL, LOCAL ? 256 : 512, LOCAL ? 256 : 512, 2>::DlaStage;
-};
+using DlaF32Stage = DlaStage<float, K, kDlaF32VS, LOCAL, LOCAL ? 256 : 512, LOCAL ? 256 : 512, 2>;
 template <int K, bool LOCAL>
 __device__ __forceinline__ void dla_f32_body(const DlaParams& p, i32x4* lds, int item, int ip) {
     typedef DlaWork<float, K, kDlaF32VS, LOCAL> Work;
@@ -736,7 +728,7 @@ __device__ __forceinline__ void dla_f32_body(const DlaParams& p, i32x4* lds, int
             int shift;
             const auto o = os.next(ch, shift);
 #pragma unroll
-            for (int vb = 0; vb < VB; ++vb) put4<float>(o, oo - shift + 64 * vb, out[vb]);
+            for (int vb = 0; vb < VB; ++vb) store16(o, oo - shift + 64 * vb, __builtin_bit_cast(i32x4, out[vb]));
             if (ch + 1 < k.c1) st.template put<1 - P>(ch + 1);
             st.template fetch<1 - P>(ch + 3);
         };
