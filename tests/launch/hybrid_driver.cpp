@@ -60,7 +60,8 @@ static int g_passes;
 // One launch of segments' own states where there are any, then one of everything.
 static void dla_seen(const Launch& l) {
     const auto& p = params<gdr2::DlaParams>(l);
-    const bool local = is(l, "ELb1E");  // <columns, LOCAL = true>
+    const bool local = is(l, "Li0ELb1") || is(l, "Li64ELb1") || is(l, "Li128ELb1");  // <row length or 0, LOCAL, ...>
+    if (is(l, "gdr2_dla_kernel")) CHECK(is(l, "ELb0ELb1E") == (p.T <= 128));         // short sequences' own variant
     const int64_t per = g_B * g_H * g_slots, n = *(int*)l.args[1];
     CHECK(is(l, "gdr2_dla_") && p.passes == g_passes && p.slots == g_slots && p.T == g_T);
     CHECK(p.segs >= 1 && p.seg_chunks >= 1 && (int64_t)p.segs * p.seg_chunks * 64 >= p.T);
