@@ -218,18 +218,36 @@ struct DlaStage {
     template <int P>
     __device__ __forceinline__ void put_z(int ch) {
         const int n = k.L - ch * C;
+        float f[ZU];
+#pragma unroll
+        for (int u = 0; u < ZU; ++u) f[u] = late[u];
+        if (n < C) {
+#pragma unroll
+            for (int u = 0; u < ZU; ++u) {
+                const int r = (zt + u * NZ) / (VS / 4);
+                f[u] = r < n ? dla_pow(k.ga, n - 1 - r) : 0.f;
+            }
+        }
+        if constexpr (ES == 2) {
+            if (exact) split_z<P, 3>(f);
+            else split_z<P, 2>(f);
+        } else {
+            split_z<P, 1>(f);
+        }
+    }
+    // z as it is, and z f in NP parts
+    template <int P, int PARTS>
+    __device__ __forceinline__ void split_z(const float (&f)[ZU]) {
 #pragma unroll
         for (int u = 0; u < ZU; ++u) {
             const int x = zt + u * NZ, r = x / (VS / 4), col = x % (VS / 4) * 4;
             const int at = tile_at<T, RZ>(r, col / E16), in = col % E16;
             if constexpr (!LOCAL) *(z4*)((T*)(t.z[P] + at) + in) = zr[P][u];
-            const float f = n >= C ? late[u] : r < n ? dla_pow(k.ga, n - 1 - r) : 0.f;
-            f32x4 rest = Raw4<T>::widen(zr[P][u]) * f;
+            f32x4 rest = Raw4<T>::widen(zr[P][u]) * f[u];
             if constexpr (ES == 2) {
                 // each time the upper eight bits of what is left: after three nothing remains of 24
 #pragma unroll
-                for (int q = 0; q < NP; ++q) {
-                    if (q == 2 && !exact) break;
+                for (int q = 0; q < PARTS; ++q) {
                     u32x2 part;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -663,7 +681,7 @@ __device__ __forceinline__ void dla_f32_body(const DlaParams& p, i32x4* lds, int
                 for (int i = 0; i < 4; ++i) k.ps.fin[k.state_at(row + i, v)] = s[i] * f;
             });
         }
-    } else {
+    } else if constexpr (!LOCAL) {
         DlaStream xs = k.rows_of_k(k.ps.x), os = k.rows_of_v(k.ps.out);
         const int xrow = 16 * w + c, xo = k.off(xrow, k.sx) + g * 16, oo = k.off(xrow, k.sz) + g * 16;
         i32x4 xr[2][KP];
