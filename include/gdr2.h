@@ -597,7 +597,8 @@ gdr2_status gdr2_dla_step(int64_t N, int64_t H, int64_t dk, int64_t dv, gdr2_dty
  * token: o is zero, nothing is stored.
  *   H a multiple of Hkv, H <= 32768, d in {64, 128}, N * H <= 2^30, B * T * Hkv <= 2^32; scale > 0, finite
  *   workspace   gdr2_paged_decode_workspace_bytes() bytes (0: none needed)
- * Precision: fp32 throughout; with GDR2_BF16 the probabilities keep 16 bits as inputs of their product.
+ * Precision: fp32 throughout; with GDR2_BF16 the probabilities keep 16 bits as inputs of their product.  A value
+ * that is not finite at a position that a token sees makes that channel of its heads infinite or NaN, no other.
  */
 gdr2_status gdr2_paged_cache_fill(int64_t B, int64_t T, int64_t Hkv, int64_t d, gdr2_dtype dtype,
                                   int64_t page, int64_t pages, int64_t width, const void* k,

@@ -422,3 +422,23 @@ def test_paged_decode_few_positions_round_once(n):
     r = hybrid.paged_decode(f64(q), f64(k), f64(v), f64(kp), f64(vp), table.tolist(), [n - 1], d ** -0.5)
     fine = swa_bounds(dict(r, lse=np.zeros(())), "f32", d, n)["o"] + 2.0 ** -16 * r["o_abs"]
     within("o", o, r["o"], fine + U["bf16"] * (1 + 2.0 ** -7) * np.abs(r["o"]))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_paged_decode_infinite_values_stay_in_their_channel(dtype):
+    gen = torch.Generator().manual_seed(3)
+    H, Hkv, d, page = 4, 2, 64, 16
+    kp, vp = randn(gen, (8, page, Hkv, d), dtype), randn(gen, (8, page, Hkv, d), dtype)
+    q, k, v = randn(gen, (2, H, d), dtype), randn(gen, (2, Hkv, d), dtype), randn(gen, (2, Hkv, d), dtype)
+    table = torch.tensor([[0, 1, 2, 3], [4, 5, 6, 7]], dtype=I32)
+    out = []
+    for bad in (False, True):
+        if bad:
+            vp[1, 3, 1, 7] = float("inf")       # sequence 0, position 19, heads 2 and 3, channel 7
+            vp[6, 0, 0, 9] = float("nan")       # sequence 1, position 32, behind its token
+            kp[6, 1, 0, 9] = float("inf")
+        kpd, vpd, qd, kd, vd, td = dev(kp, vp, q, k, v, table)
+        out.append(g2.gdr2_paged_decode_step(qd, kd, vd, kpd, vpd, td, i32([40, 31])).cpu())
+    same = torch.ones_like(out[0], dtype=torch.bool)
+    same[0, 2:, 7] = False
+    assert torch.equal(out[0][same], out[1][same]) and not torch.isfinite(out[1][~same]).any()

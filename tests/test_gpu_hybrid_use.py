@@ -336,6 +336,27 @@ def test_linear_attention_past_31_bits():
     assert torch.equal(o[-2:], o2) and torch.equal(S[-2:], S2)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_linear_attention_of_the_most_heads(dtype):
+    """Rows 2^15 heads apart (a chunk of 64 spans a gigabyte in fp32): heads at both ends equal those heads alone."""
+    T, H, dk, dv = 130, 32768, 64, 64
+    announce(f"linear attention of {H} heads, {dtype}")
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    q, k, v = (torch.empty(1, T, H, dk, dtype=dt, device=DEV).normal_() for _ in range(3))
+    g = -0.1 * torch.rand(H, device=DEV)
+    L = _i32([129])
+    pick = [0, 1, H // 2, H - 1]
+    few = lambda t: t[:, :, pick].contiguous()  # noqa: E731
+    o, S = g2.gdr2_dla_fwd(q, k, v, g, lengths=L)
+    o2, S2 = g2.gdr2_dla_fwd(few(q), few(k), few(v), g[pick].contiguous(), lengths=L)
+    assert torch.equal(o[:, :, pick], o2) and torch.equal(S[:, pick], S2)
+    gr = g2.gdr2_dla_bwd(q, k, v, g, v, lengths=L)
+    g2r = g2.gdr2_dla_bwd(few(q), few(k), few(v), g[pick].contiguous(), few(v), lengths=L)
+    for n in ("dq", "dk", "dv"):
+        assert torch.equal(gr[n][:, :, pick], g2r[n]), n
+    assert torch.equal(gr["dS0"][:, pick], g2r["dS0"])
+
+
 def test_pages_past_31_bits():
     pages, page, Hkv, d = 72000, 64, 4, 128
     announce(f"pages of {pages * page * Hkv * d} elements")
