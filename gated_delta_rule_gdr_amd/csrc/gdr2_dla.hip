@@ -8,23 +8,21 @@
 // kept by the forward.  Chunks of 64 tokens: inside a chunk through the scores x_r . y_s, weighted a^(r - s);
 // from before it through the state, out_r += a^(r + 1) x_r S; then S <- a^64 S + sum_s a^(63 - s) y_s z_s^T.
 //
-// A workgroup carries some columns of one chain's state in fp32 registers (columns are independent), over the
-// whole sequence or, where there are few chains, over one segment of it, whose entering state is put together from
+// A workgroup carries the columns of one chain's state (fp32: 32 of them; columns are independent) in fp32 registers,
+// over the whole sequence or, where there are few chains, over one segment of it, whose entering state is put together from
 // the segments' own states (a first launch).  Scores are formed transposed (rows s, columns r), so that a lane's
-// weighted scores are operand values of the next product as they stand; the state is read from a copy in LDS (bf16: rounded)
-// that each chunk writes for the next one.
+// weighted scores are operand values of the next product as they stand, and so are its values of the state.
 //
 // Rounding: S is carried in fp32, its decay as S + S (a^n - 1), so that slow decays lose nothing over long
 // sequences.  For bf16 the decayed operand of its sums is split into bf16 parts: three (24 bits) where the state is a
-// result, two where it is only read, as bf16 (the third costs 3 % of a backward).  Scores, and S as it is read, are
-// rounded to bf16 once as inputs of their products (in short sequences: split in two), whose sums are fp32.  fp32 rounds
-// nothing else.
+// result, two where it is only read, as bf16.  Scores, and S as it is read, are rounded to bf16 once as inputs of their
+// products (in short sequences: split in two), whose sums are fp32.  fp32 rounds nothing else.
 //
-// Measured (dk = dv = 128, bf16): B = 4, T = 4096, H = 16 forward 114 us (1.2 TB/s of its rows), backward 200 us (its
-// tensors, each once, would take 84 us; products 31 us); B = 1, T = 32768, H = 16 with its states 210 us.  The chain of steps
-// inside a chunk bounds it: scores wait for rows, products for scores, the next tiles for the products; a chunk takes 2.3 us
-// alone on a compute unit, two at once 3.5 us, with the matrix units a quarter busy, LDS a third, the caches' port a
-// third.  fp32 (B = 3, T = 777, H = 6, dk = 64, dv = 128): forward 29 us, backward 76 us, bound by the fp32 matrix rate: the
+// Measured (dk = dv = 128, bf16): B = 4, T = 4096, H = 16 forward 103 us, backward 176 us (its tensors, each once, take 94
+// us at a copy's rate, its 99 GFLOP of products 80 us at the rate of a large one); B = 1, T = 32768, H = 16 195 us, the
+// bytes of its two launches 168 us.  The chain of steps inside a chunk bounds the backward: the owners' 54 products of 32
+// cycles wait for operands from LDS, each other and two barriers, 5600 cycles a chunk; LDS and the matrix units are 30 % busy.
+// fp32 (B = 3, T = 777, H = 6, dk = 64, dv = 128): forward 29 us, backward 76 us, bound by the fp32 matrix rate: the
 // busiest of four SIMDs has 288 products of 32 cycles per chunk, 9200 of its 13000 cycles.
 #include "gdr2_common.hpp"
 #include "gdr2_hybrid_kernels.hpp"
@@ -32,14 +30,14 @@
 namespace gdr2 {
 
 constexpr int kDlaThreads = 256, C = kDlaChunk;
-// Columns of a workgroup's state.  bf16: scores are formed again for every 64, and 64 is what registers hold with two
-// workgroups to a compute unit; with 32, forward and backward of B = 4, T = 4096, H = 16 took 361 us against 331, a prompt of
-// 32768 289 against 222.  fp32: 64 would leave no register for the rows ahead.
-constexpr int kDlaVS = 64, kDlaF32VS = 32;
+// Columns of an fp32 workgroup's state: 64 would leave no register for the rows ahead.  (bf16 takes all columns: with 64 to
+// a workgroup, two waves for the outputs, two for the state and that read from LDS, two workgroups to a compute unit, forward
+// and backward of B = 4, T = 4096, H = 16 took 112 + 198 us against 103 + 176, a prompt of 32768 207 against 195.)
+constexpr int kDlaF32VS = 32;
 // Up to this length bf16 keeps 16 bits of the scores and of the state as it is read (two products each): sums that short do
 // not average roundings out.  Normwise error over that of the exact result rounded once, 1 to 64 tokens of a few
 // heads: 1.0 against up to 1.96; from 129 tokens on it is 1.41 to 1.44 with one rounding each.  It costs 64 prompts of 128 tokens
-// (H = 16, dk = dv = 128) 66 us for 59, their backward 144 for 123; fewer chains less than a microsecond.
+// (H = 16, dk = dv = 128) 67 us for 60, their backward 133 for 119; fewer chains less than a microsecond.
 constexpr int kDlaFine = 128;
 
 // a^n for whole n >= 0; a^0 = 1 also where a = 0
@@ -68,11 +66,6 @@ __device__ __forceinline__ i32x4 load16(__amdgpu_buffer_rsrc_t t, int offset) {
 }
 __device__ __forceinline__ void store16(__amdgpu_buffer_rsrc_t t, int offset, const i32x4& v) {
     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), t, offset, 0, 0);
-}
-template <typename T>
-__device__ __forceinline__ typename Raw4<T>::t load4(__amdgpu_buffer_rsrc_t t, int offset) {
-    if constexpr (sizeof(T) == 2) return __builtin_bit_cast(bf16x4, __builtin_amdgcn_raw_buffer_load_b64(t, offset, 0, 0));
-    else return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(t, offset, 0, 0));
 }
 __device__ __forceinline__ float uniform(float x) {
     return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, x)));
@@ -159,123 +152,6 @@ struct DlaWork {
     }
 };
 
-// Staging of y (16 bytes at a time, by NY threads) and z (four columns at a time, by NZ), z also as the decayed operand
-// z_s a^(63 - s) of the state's sums: for bf16 in parts of 8 bits each, three where the state is a result, two where it is only
-// read as bf16.  With two buffers (NB) set (ch - c0) % 2 of the registers and of the tiles belongs to chunk ch.  Behind
-// the last chunk nothing is loaded.
-template <typename T, int K, int VS, bool LOCAL, int NY, int NZ, int NB>
-struct DlaStage {
-    typedef DlaWork<T, K, VS, LOCAL> Work;
-    typedef typename Raw4<T>::t z4;
-    static constexpr int ES = Work::ES, E16 = Work::E16, RY = Work::RY, RZ = Work::RZ;
-    static constexpr int YU = C * RY / NY, ZU = C * VS / 4 / NZ, NP = ES == 2 ? 3 : 1;
-    static constexpr int RS = ES == 2 ? RY + 1 : RY;  // pieces of a row of the state (bf16: read along rows only, padded by one)
-    static_assert(YU >= 1 && ZU >= 1, "staging");
-    struct Tiles {
-        i32x4 y[NB][C * RY];
-        i32x4 z[LOCAL ? 1 : NB][LOCAL ? 1 : C * RZ];
-        i32x4 d[NB][NP][C * RZ];
-        i32x4 s[LOCAL ? 1 : NB][LOCAL ? 1 : VS * RS];  // the state as the chunk reads it, [v][k]
-    };
-    const Work& k;
-    Tiles& t;
-    DlaStream ys, zs;
-    i32x4 yr[NB][YU];
-    z4 zr[NB][ZU];
-    int yt, zt, yo[YU], zo[ZU];
-    float late[ZU];  // a^(63 - s) of the staged rows
-    bool exact;      // the third part too
-    __device__ __forceinline__ DlaStage(const Work& work, Tiles& tiles, int ythread, int zthread)
-        : k(work), t(tiles), ys(work.rows_of_k(work.ps.y)), zs(work.rows_of_v(work.ps.z)), yt(ythread), zt(zthread), exact(work.ps.state && (LOCAL || work.final_here())) {
-#pragma unroll
-        for (int u = 0; u < YU; ++u) yo[u] = k.off((yt + u * NY) / RY, k.sx) + (yt + u * NY) % RY * 16;
-#pragma unroll
-        for (int u = 0; u < ZU; ++u) {
-            const int x = zt + u * NZ, r = x / (VS / 4);
-            zo[u] = k.off(r, k.sz) + x % (VS / 4) * 4 * ES;
-            late[u] = dla_pow(k.ga, C - 1 - r);
-        }
-    }
-    template <int P>
-    __device__ __forceinline__ void fetch_y(int ch) {
-        int shift;
-        const auto y = ys.next(ch, shift);
-#pragma unroll
-        for (int u = 0; u < YU; ++u) yr[P][u] = load16(y, yo[u] - shift);
-    }
-    template <int P>
-    __device__ __forceinline__ void fetch_z(int ch) {
-        int shift;
-        const auto z = zs.next(ch, shift);
-#pragma unroll
-        for (int u = 0; u < ZU; ++u) zr[P][u] = load4<T>(z, zo[u] - shift);
-    }
-    template <int P>
-    __device__ __forceinline__ void put_y() {
-#pragma unroll
-        for (int u = 0; u < YU; ++u) t.y[P][tile_at<T, RY>((yt + u * NY) / RY, (yt + u * NY) % RY)] = yr[P][u];
-    }
-    template <int P>
-    __device__ __forceinline__ void put_z(int ch) {
-        const int n = k.L - ch * C;
-        float f[ZU];
-#pragma unroll
-        for (int u = 0; u < ZU; ++u) f[u] = late[u];
-        if (n < C) {
-#pragma unroll
-            for (int u = 0; u < ZU; ++u) {
-                const int r = (zt + u * NZ) / (VS / 4);
-                f[u] = r < n ? dla_pow(k.ga, n - 1 - r) : 0.f;
-            }
-        }
-        if constexpr (ES == 2) {
-            if (exact) split_z<P, 3>(f);
-            else split_z<P, 2>(f);
-        } else {
-            split_z<P, 1>(f);
-        }
-    }
-    // z as it is, and z f in NP parts
-    template <int P, int PARTS>
-    __device__ __forceinline__ void split_z(const float (&f)[ZU]) {
-#pragma unroll
-        for (int u = 0; u < ZU; ++u) {
-            const int x = zt + u * NZ, r = x / (VS / 4), col = x % (VS / 4) * 4;
-            const int at = tile_at<T, RZ>(r, col / E16), in = col % E16;
-            if constexpr (!LOCAL) *(z4*)((T*)(t.z[P] + at) + in) = zr[P][u];
-            f32x4 rest = Raw4<T>::widen(zr[P][u]) * f[u];
-            if constexpr (ES == 2) {
-                // each time the upper eight bits of what is left: after three nothing remains of 24
-#pragma unroll
-                for (int q = 0; q < PARTS; ++q) {
-                    u32x2 part;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float even = rest[2 * i], odd = rest[2 * i + 1];
-                        const unsigned lo = __builtin_bit_cast(unsigned, even), hi = __builtin_bit_cast(unsigned, odd);
-                        part[i] = __builtin_amdgcn_perm(hi, lo, 0x07060302);
-                        rest[2 * i] = even - __builtin_bit_cast(float, lo & 0xffff0000u);
-                        rest[2 * i + 1] = odd - __builtin_bit_cast(float, hi & 0xffff0000u);
-                    }
-                    *(u32x2*)((T*)(t.d[P][q] + at) + in) = part;
-                }
-            } else {
-                *(f32x4*)(t.d[P][0] + at) = rest;
-            }
-        }
-    }
-    template <int P>
-    __device__ __forceinline__ void fetch(int ch) {
-        fetch_y<P>(ch);
-        fetch_z<P>(ch);
-    }
-    template <int P>
-    __device__ __forceinline__ void put(int ch) {
-        put_y<P>();
-        put_z<P>(ch);
-    }
-};
-
 // The workgroup's share of the launch goes to `body` with the length of its pass' rows: KM, or (KM = 0, dk and dv differ in
 // a backward) the pass' own.
 template <int KM, typename F>
@@ -290,9 +166,12 @@ __device__ __forceinline__ void dla_share(const DlaParams& p, int nwork, F&& bod
 }
 
 // ------------------------------------------------------------------ bf16
-// 32 x 32 products over 64 columns.  Two waves read: outputs of 32 rows each.  Two carry the state: every other 32 of its
-// rows.  They run loops of their own that meet at two barriers per chunk, before and behind the products; between the second
-// and the next first the next chunk's tiles are written.  (For a segment's own state alone, LOCAL, all four carry.)
+// 32 x 32 products.  A workgroup takes all columns of a pass: a wave per 32 of them owns their state and outputs, and four
+// waves help: they bring the tiles, a chunk ahead, and form the scores, a block of 32 x 32 each of three.  Loops of
+// their own meet at two barriers per chunk: before the first the owners read the state and carry it on while the helpers
+// form this chunk's scores and write the next one's rows; behind it the owners add the scores' part and store, and the helpers
+// write the next decayed operand.  (For a segment's own state alone, LOCAL, one barrier.)
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 __device__ __forceinline__ int acc_row32(int i, int l) { return 8 * (i / 4) + 4 * (l >> 5) + i % 4; }
 // operand of 32 columns from piece q of a tile, contraction down sixteen rows from r0: rows 4 h .. + 3 and 8 + 4 h .. + 3
 template <int R>
@@ -302,55 +181,95 @@ __device__ __forceinline__ bf16x8 columns32(const i32x4* t, int r0, int q, int l
     const bf16x4 hi = ds_read_tr4((const bf16*)(t + tile_at<bf16, R>(row + 8, piece)) + 4 * (p & 1));
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 __device__ __forceinline__ void mma32x32(f32x16& c, const bf16x8& a, const bf16x8& b) {
     c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 __device__ __forceinline__ f32x16 zeros16() { return f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0}; }
 
-template <int K, bool LOCAL>
-struct DlaLds {
-    typedef DlaStage<bf16, K, kDlaVS, LOCAL, LOCAL ? 256 : 128, 256, 1> Stage;
-    typename Stage::Tiles t;
-    i32x4 own[LOCAL ? 1 : 2][32 * 9];  // a reading wave's own: 64 channels of its rows, or its outputs
+constexpr int kDlaHelp = 256;  // the helpers' threads
+// Two buffers belong to chunks by turns.
+template <int K, int V, bool LOCAL, bool FINE>
+struct DlaTiles {
+    i32x4 y[2][C * K / 8];
+    i32x4 x[LOCAL ? 1 : 2][LOCAL ? 1 : C * K / 8];
+    i32x4 z[LOCAL ? 1 : 2][LOCAL ? 1 : C * V / 8];
+    i32x4 d[LOCAL ? 2 : 1][3][C * V / 8];                // z_s a^(63 - s) in parts of 8 bits
+    i32x4 pr[FINE ? 2 : 1][LOCAL ? 1 : 6 * 64];          // weighted scores, as the owners' lanes take them
 };
-// FINE: scores and the state as it is read in two parts each; the state's second part takes the first one's place in LDS
-// between two more barriers.
-template <int K, bool LOCAL, bool FINE>
+
+// A helper's share of the rows of one tensor: 16 bytes at a time.
+template <int R>
+struct DlaRows {
+    static constexpr int U = C * R / kDlaHelp;
+    DlaStream s;
+    int off[U];
+    i32x4 r[U];
+    template <typename W>
+    __device__ __forceinline__ DlaRows(const W& k, const DlaStream& stream, int stride, int th) : s(stream) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) off[u] = k.off((th + u * kDlaHelp) / R, stride) + (th + u * kDlaHelp) % R * 16;
+    }
+    __device__ __forceinline__ void fetch(int ch) {
+        int shift;
+        const auto t = s.next(ch, shift);
+#pragma unroll
+        for (int u = 0; u < U; ++u) r[u] = load16(t, off[u] - shift);
+    }
+    // pieces 2 i and 2 i + 1 as their first halves and their second ones
+    __device__ __forceinline__ void put_halves(i32x4* tile, int th) const {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int row = (th + u * kDlaHelp) / R, piece = (th + u * kDlaHelp) % R, even = piece & ~1;
+            *((u32x2*)(tile + tile_at<bf16, R>(row, even)) + (piece & 1)) = u32x2{(unsigned)r[u][0], (unsigned)r[u][1]};
+            *((u32x2*)(tile + tile_at<bf16, R>(row, even + 1)) + (piece & 1)) = u32x2{(unsigned)r[u][2], (unsigned)r[u][3]};
+        }
+    }
+    __device__ __forceinline__ void put(i32x4* tile, int th) const {
+#pragma unroll
+        for (int u = 0; u < U; ++u) tile[tile_at<bf16, R>((th + u * kDlaHelp) / R, (th + u * kDlaHelp) % R)] = r[u];
+    }
+};
+// f times two values, in parts: each time the upper eight bits of what is left; after three nothing remains of 24.
+__device__ __forceinline__ void split2(int two, float f, int& p0, int& p1, int& p2) {
+    auto upper = [](float x) { return __builtin_bit_cast(float, __builtin_bit_cast(unsigned, x) & 0xffff0000u); };
+    auto pair = [](float lo, float hi) { return (int)__builtin_amdgcn_perm(__builtin_bit_cast(unsigned, hi), __builtin_bit_cast(unsigned, lo), 0x07060302); };
+    float lo = __builtin_bit_cast(float, (unsigned)two << 16) * f, hi = __builtin_bit_cast(float, (unsigned)two & 0xffff0000u) * f;
+    p0 = pair(lo, hi);
+    lo -= upper(lo), hi -= upper(hi);
+    p1 = pair(lo, hi);
+    lo -= upper(lo), hi -= upper(hi);
+    p2 = pair(lo, hi);
+}
+
+template <int K, int V, bool LOCAL, bool FINE>
 __device__ __forceinline__ void dla_body(const DlaParams& p, i32x4* lds, int item, int ip) {
-    typedef DlaWork<bf16, K, kDlaVS, LOCAL> Work;
-    typedef typename DlaLds<K, LOCAL>::Stage Stage;
-    constexpr int KK = K / 16, RY = Work::RY, RZ = Work::RZ, VB = kDlaVS / 32;
-    // carrying waves, and the blocks of 32 x 32 of each: rows cw % NK + NK kb, columns cv + vb (times 32)
-    constexpr int NW = LOCAL ? 4 : 2, NK = NW < K / 32 ? NW : K / 32, KB = K / 32 / NK, CB = VB * NK / NW;
-    auto& t = ((DlaLds<K, LOCAL>*)lds)->t;
+    typedef DlaWork<bf16, K, V, LOCAL> Work;
+    constexpr int KK = K / 16, KB = K / 32, VB = V / 32, RK = K / 8, RV = V / 8;
+    auto& t = *(DlaTiles<K, V, LOCAL, FINE>*)lds;
+    const int l = lane_id(), w = __builtin_amdgcn_readfirstlane(wave_id()), n = l & 31, hf = l >> 5;
+    if (w >= kDlaHelp / 64 + VB) return;  // a launch for wider passes too
     const Work k(p, item, ip);
     if (LOCAL && k.c1 - k.c0 < p.seg_chunks) return;  // no later segment has a token: nobody reads this one's state
-    const int l = lane_id(), w = __builtin_amdgcn_readfirstlane(wave_id()), n = l & 31, hf = l >> 5;
-    Stage st(k, t, (int)threadIdx.x - (LOCAL ? 0 : 128), threadIdx.x);
-    if (LOCAL || w >= 2) {
-        const int cw = LOCAL ? w : w - 2, ck = cw % NK, cv = cw / NK * CB;
-        f32x16 S[KB][CB];  // rows 32 (ck + NK kb) + acc_row32(i), columns 32 (cv + vb) + n
-        auto each_block = [&](auto&& f) {
+    const bool exact = k.ps.state && (LOCAL || k.final_here());
+    auto owner = [&](auto parts) {
+        constexpr int PARTS = decltype(parts)::value;
+        const int cv = w - kDlaHelp / 64;
+        f32x16 S[KB];  // rows 32 kb + acc_row32(i), columns 32 cv + n
+        auto each_four = [&](int j, auto&& f) {  // of the own state of segment j
+            f32x4* at = (f32x4*)k.local(j) + l;
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-                for (int vb = 0; vb < CB; ++vb) f(S[kb][vb], ck + NK * kb, cv + vb);
+                for (int i = 0; i < 4; ++i) f(S[kb], 4 * i, at[((kb * VB + cv) * 4 + i) * 64]);
         };
-        auto each_four = [&](int j, auto&& f) {  // of the own state of segment j
-            f32x4* at = (f32x4*)k.local(j) + l;
-            each_block([&](f32x16& s, int kb, int vb) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) f(s, 4 * i, at[((kb * VB + vb) * 4 + i) * 64]);
-            });
-        };
-        each_block([&](f32x16& s, int, int) { s = zeros16(); });
+        for (int kb = 0; kb < KB; ++kb) S[kb] = zeros16();
         if constexpr (!LOCAL) {
             if (k.ps.init)
-                each_block([&](f32x16& s, int kb, int vb) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) s[i] = k.ps.init[k.state_at(32 * kb + acc_row32(i, l), 32 * vb + n)];
-                });
+                for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) S[kb][i] = k.ps.init[k.state_at(32 * kb + acc_row32(i, l), 32 * cv + n)];
             for (int j = 0; j < k.sg && k.c0 < k.nch; ++j) {
                 const float e = expm1f((float)(p.seg_chunks * C - (j == 0 ? k.early : 0)) * k.ga);
                 each_four(j, [&](f32x16& s, int i0, const f32x4& x) {
@@ -359,228 +278,315 @@ __device__ __forceinline__ void dla_body(const DlaParams& p, i32x4* lds, int ite
                 });
             }
         }
-        auto put_state = [&]() {
-            if constexpr (!LOCAL)
-                each_block([&](const f32x16& s, int kb, int vb) {
+        DlaStream os = k.rows_of_v(k.ps.out);
+        int oo[2];
+        float before[2], before0[2];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        store4((bf16*)(t.s[0] + (32 * vb + n) * Stage::RS + 4 * kb + i) + 4 * hf, f32x4{s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]});
-                });
-        };
-        auto put_rest = [&]() {  // what rounding left of it
-            each_block([&](const f32x16& s, int kb, int vb) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    f32x4 r;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) r[e] = s[4 * i + e] - (float)(bf16)s[4 * i + e];
-                    store4((bf16*)(t.s[0] + (32 * vb + n) * Stage::RS + 4 * kb + i) + 4 * hf, r);
-                }
-            });
-        };
-        const float whole = expm1f((float)C * k.ga);
-        if (k.c0 < k.c1) {
-            st.template fetch<0>(k.c0);
-            put_state();
-            st.template put<0>(k.c0);
-            st.template fetch<0>(k.c0 + 1);
+        for (int rb = 0; rb < 2; ++rb) {
+            const int r = 32 * rb + n;
+            oo[rb] = k.off(r, k.sz) + (32 * cv + 8 * hf) * 2;
+            before[rb] = dla_pow(k.ga, r + 1);
+            before0[rb] = k.early ? dla_pow(k.ga, r) : before[rb];
         }
+        const float whole = expm1f((float)C * k.ga);
+        if (k.c0 < k.c1) lds_barrier();
         for (int ch = k.c0; ch < k.c1; ++ch) {
-            lds_barrier();
-            if constexpr (FINE) {
-                lds_barrier();
-                put_rest();
-                lds_barrier();
-            }
-            const float e = k.decay(ch, whole);
-            each_block([&](f32x16& s, int, int) {
+            const int P = (ch - k.c0) & 1;
+            f32x16 out[2];
+            if constexpr (!LOCAL) {
+                // from before the chunk: out^T = S^T x, rows v, columns r.  A lane's values of S are operand values as they
+                // stand, contraction rows 4 h .. + 3 and 8 + 4 h .. + 3 of sixteen; x is read in that order.
+                out[0] = out[1] = zeros16();
+                bf16x8 xb[2][2];
+                auto takex = [&](int kk) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) s[i] = fmaf(s[i], e, s[i]);
-            });
+                    for (int rb = 0; rb < 2; ++rb) xb[kk % 2][rb] = __builtin_bit_cast(bf16x8, t.x[P][tile_at<bf16, RK>(32 * rb + n, 2 * kk + hf)]);
+                };
+                takex(0);
 #pragma unroll
-            for (int kk = 0; kk < C / 16; ++kk) {
-                bf16x8 y[KB];
+                for (int kk = 0; kk < KK; ++kk) {
+                    if (kk + 1 < KK) takex(kk + 1);
+                    __builtin_amdgcn_sched_barrier(0);
+                    bf16x8 s, rest;
 #pragma unroll
-                for (int kb = 0; kb < KB; ++kb) y[kb] = columns32<RY>(t.y[0], 16 * kk, 4 * (ck + NK * kb), l);
+                    for (int e = 0; e < 8; ++e) {
+                        const float v = S[kk / 2][8 * (kk % 2) + e];
+                        s[e] = (bf16)v;
+                        if constexpr (FINE) rest[e] = (bf16)(v - (float)s[e]);
+                    }
 #pragma unroll
-                for (int q = 0; q < Stage::NP; ++q) {
-                    if (q == 2 && !st.exact) break;
-#pragma unroll
-                    for (int vb = 0; vb < CB; ++vb) {
-                        const bf16x8 z = columns32<RZ>(t.d[0][q], 16 * kk, 4 * (cv + vb), l);
-#pragma unroll
-                        for (int kb = 0; kb < KB; ++kb) mma32x32(S[kb][vb], y[kb], z);
+                    for (int rb = 0; rb < 2; ++rb) {
+                        mma32x32(out[rb], s, xb[kk % 2][rb]);
+                        if constexpr (FINE) mma32x32(out[rb], rest, xb[kk % 2][rb]);
                     }
                 }
             }
-            if (ch + 1 < k.c1) {
-                lds_barrier();
-                put_state();
-                st.template put<0>(ch + 1);
-                st.template fetch<0>(ch + 2);
+            const float e = k.decay(ch, whole);
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) S[kb][i] = fmaf(S[kb][i], e, S[kb][i]);
+            bf16x8 y[2][KB], d[2][PARTS];  // operands a step ahead
+            auto take = [&](int kk) {
+#pragma unroll
+                for (int q = 0; q < PARTS; ++q) d[kk % 2][q] = columns32<RV>(t.d[LOCAL ? P : 0][q], 16 * kk, 4 * cv, l);
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) y[kk % 2][kb] = columns32<RK>(t.y[P], 16 * kk, 4 * kb, l);
+            };
+            take(0);
+#pragma unroll
+            for (int kk = 0; kk < C / 16; ++kk) {
+                if (kk + 1 < C / 16) take(kk + 1);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int q = 0; q < PARTS; ++q)
+#pragma unroll
+                    for (int kb = 0; kb < KB; ++kb) mma32x32(S[kb], y[kk % 2][kb], d[kk % 2][q]);
             }
+            if constexpr (!LOCAL) {
+#pragma unroll
+                for (int rb = 0; rb < 2; ++rb) {
+                    const float f = ch == 0 ? before0[rb] : before[rb];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) out[rb][i] *= f;
+                }
+                lds_barrier();
+                // out^T += z^T scores^T: rows s of the first half for both halves of r, of the second for the second
+#pragma unroll
+                for (int kk = 0; kk < C / 16; ++kk) {
+                    const bf16x8 z = columns32<RV>(t.z[P], 16 * kk, 4 * cv, l);
+#pragma unroll
+                    for (int q = 0; q < (FINE ? 2 : 1); ++q) {
+                        if (kk < 2) mma32x32(out[0], z, __builtin_bit_cast(bf16x8, t.pr[q][kk * 64 + l]));
+                        mma32x32(out[1], z, __builtin_bit_cast(bf16x8, t.pr[q][((kk < 2 ? 4 : 2) + kk % 2) * 64 + l]));
+                    }
+                }
+                int shift;
+                const auto o = os.next(ch, shift);
+#pragma unroll
+                for (int rb = 0; rb < 2; ++rb)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        // lanes n and n + 32 hold fours of columns in turn: exchanged, each has eight in a row
+                        const f32x16& v = out[rb];
+                        const u32x2 a = __builtin_bit_cast(u32x2, Raw4<bf16>::narrow(f32x4{v[8 * m], v[8 * m + 1], v[8 * m + 2], v[8 * m + 3]}));
+                        const u32x2 b = __builtin_bit_cast(u32x2, Raw4<bf16>::narrow(f32x4{v[8 * m + 4], v[8 * m + 5], v[8 * m + 6], v[8 * m + 7]}));
+                        const auto p0 = __builtin_amdgcn_permlane32_swap(a[0], b[0], false, false), p1 = __builtin_amdgcn_permlane32_swap(a[1], b[1], false, false);
+                        store16(o, oo[rb] - shift + 32 * m, i32x4{(int)p0[0], (int)p1[0], (int)p0[1], (int)p1[1]});
+                    }
+            }
+            if (ch + 1 < k.c1) lds_barrier();
         }
         if constexpr (LOCAL) {
             each_four(k.sg, [&](const f32x16& s, int i0, f32x4& x) { x = f32x4{s[i0], s[i0 + 1], s[i0 + 2], s[i0 + 3]}; });
         } else if (k.ps.fin && k.final_here()) {
             // against time the final state is decayed once more (dS0 = a R_0)
             const float f = k.rev && k.L > 0 ? dla_pow(k.ga, 1) : 1.f;
-            each_block([&](const f32x16& s, int kb, int vb) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) k.ps.fin[k.state_at(32 * kb + acc_row32(i, l), 32 * vb + n)] = s[i] * f;
-            });
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) k.ps.fin[k.state_at(32 * kb + acc_row32(i, l), 32 * cv + n)] = S[kb][i] * f;
         }
+    };
+    if (w >= kDlaHelp / 64) {
+        if (exact) owner(IC<3>{});
+        else owner(IC<2>{});
     } else {
-        // The wave's 32 rows arrive as whole lines (a lane's own pieces, as the products want them, would be 32 lines a
-        // load), and outputs leave so; both turn round in the wave's own LDS.
-        DlaStream xs = k.rows_of_k(k.ps.x), os = k.rows_of_v(k.ps.out);
-        i32x4* own = ((DlaLds<K, LOCAL>*)lds)->own[w];
-        constexpr int XR = 8, XH = K / 64;  // pieces of a row and rounds: 64 channels at a time
-        const int xrow = 32 * w + n;
-        const int xo = k.off(32 * w + l / XR, k.sx) + l % XR * 16, oo = k.off(32 * w + l / RZ, k.sz) + l % RZ * 16;
-        const int xd = k.rev ? -8 * k.sx : 8 * k.sx, od = k.rev ? -8 * k.sz : 8 * k.sz;  // eight rows on
-        int at[KK];  // row n of a tile, the lane's piece
+        const int th = threadIdx.x;
+        DlaRows<RK> xs(k, k.rows_of_k(k.ps.x), k.sx, th), ys(k, k.rows_of_k(k.ps.y), k.sx, th);
+        DlaRows<RV> zs(k, k.rows_of_v(k.ps.z), k.sz, th);
+        constexpr int ZU = DlaRows<RV>::U;
+        float late[ZU];  // a^(63 - s) of the own rows of z
 #pragma unroll
-        for (int kk = 0; kk < KK; ++kk) at[kk] = tile_at<bf16, RY>(n, 2 * kk + hf);
-        i32x4 xp[XH][4], xr[KK];
-        auto fetch_x = [&](int ch) {
-            int shift;
-            const auto x = xs.next(ch, shift);
-#pragma unroll
-            for (int q = 0; q < XH; ++q)
-#pragma unroll
-                for (int u = 0; u < 4; ++u) xp[q][u] = load16(x, xo + (xd * u - shift) + q * 128);
-        };
-        auto take_x = [&]() {
-#pragma unroll
-            for (int q = 0; q < XH; ++q) {
-                wave_sync();
-#pragma unroll
-                for (int u = 0; u < 4; ++u) own[(8 * u + l / XR) * (XR + 1) + l % XR] = xp[q][u];
-                wave_sync();
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) xr[4 * q + kk] = own[n * (XR + 1) + 2 * kk + hf];
+        for (int u = 0; u < ZU; ++u) late[u] = dla_pow(k.ga, C - 1 - (th + u * kDlaHelp) / RV);
+        auto put_rows = [&](int P) {
+            ys.put(t.y[P], th);
+            if constexpr (!LOCAL) {
+                xs.put_halves(t.x[P], th);
+                zs.put(t.z[P], th);
             }
         };
-        auto put_out = [&](int ch, const f32x16 (&out)[VB]) {
-            static_assert(RZ == XR, "outputs turn round in the rows' place");
-            wave_sync();
-#pragma unroll
-            for (int vb = 0; vb < VB; ++vb)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    store4((bf16*)(own + n * (XR + 1) + 4 * vb + i) + 4 * hf, f32x4{out[vb][4 * i], out[vb][4 * i + 1], out[vb][4 * i + 2], out[vb][4 * i + 3]});
-            wave_sync();
-            int shift;
-            const auto o = os.next(ch, shift);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) store16(o, oo + (od * u - shift), own[(8 * u + l / XR) * (XR + 1) + l % XR]);
+        auto fetch_rows = [&](int ch) {  // all but z, which the decayed operand is still formed from
+            if constexpr (!LOCAL) xs.fetch(ch);
+            ys.fetch(ch);
         };
-        // Weights that every chunk shares: a^(r - s) inside the wave's 32 rows and to the 32 before them.  The lane's values
-        // 4 j .. 4 j + 3 of a block are rows s = s_j .. s_j + 3, so a^(r - s) is a^(r - s_j - 3) times a^3, a^2, a, 1; both are
-        // powers with an exponent >= 0 but where the diagonal passes through the four, which have weights of their own.
-        float self[4], prev[4], diag[4];
+        i32x4 part0[ZU], part1[ZU], part2[ZU];
+        auto split_late = [&](int ch) {
+            const int m = k.L - ch * C;
+            float f[ZU];
+#pragma unroll
+            for (int u = 0; u < ZU; ++u) f[u] = late[u];
+            if (m < C) {
+#pragma unroll
+                for (int u = 0; u < ZU; ++u) {
+                    const int r = (th + u * kDlaHelp) / RV;
+                    f[u] = r < m ? dla_pow(k.ga, m - 1 - r) : 0.f;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < ZU; ++u) {
+                int a[4], b[4], c[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) split2(zs.r[u][i], f[u], a[i], b[i], c[i]);
+                part0[u] = i32x4{a[0], a[1], a[2], a[3]};
+                part1[u] = i32x4{b[0], b[1], b[2], b[3]};
+                part2[u] = i32x4{c[0], c[1], c[2], c[3]};
+            }
+        };
+        auto put_late = [&](int P) {
+#pragma unroll
+            for (int u = 0; u < ZU; ++u) {
+                const int at = tile_at<bf16, RV>((th + u * kDlaHelp) / RV, (th + u * kDlaHelp) % RV);
+                t.d[P][0][at] = part0[u];
+                t.d[P][1][at] = part1[u];
+                if (exact) t.d[P][2][at] = part2[u];
+            }
+        };
+        // Scores: waves 0 and 1 the blocks on the diagonal (rows r and s from 32 w), wave 2 the one before the second.  The lane's
+        // values 4 j .. 4 j + 3 of a block are rows s = s_j .. s_j + 3 of column r, so a^(r - s) is a^(r - s_j - 3) times a^3, a^2,
+        // a, 1; both are powers with an exponent >= 0 but where the diagonal passes through the four, which have weights of
+        // their own.
+        const int first = n - 4 * hf;     // r - s_0 on the diagonal
+        const int xb = w == 0 ? 0 : 32, yb = w == 1 ? 32 : 0;
+        float near[4], diag[4];
         const float a1 = uniform(dla_pow(k.ga, 1)), a2 = uniform(dla_pow(k.ga, 2)), a3 = uniform(dla_pow(k.ga, 3));
         const float fall[4] = {a3, a2, a1, 1.f};
-        const int first = n - 4 * hf;     // r - s_0
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            self[j] = first - 8 * j < 3 ? 0.f : dla_pow(k.ga, first - 8 * j - 3);
-            prev[j] = dla_pow(k.ga, first - 8 * j + 29);
+            const int least = first + (w == 2 ? 32 : 0) - 8 * j - 3;
+            near[j] = least < 0 ? 0.f : dla_pow(k.ga, least);
             const int lag = (n & 7) - 4 * hf - j;
             diag[j] = lag < 0 ? 0.f : dla_pow(k.ga, lag);
         }
-        const int on = first < 0 || first % 8 > 2 ? -1 : first / 8;  // the four that the diagonal leaves in part
-        const float before = dla_pow(k.ga, xrow + 1), before0 = k.early ? dla_pow(k.ga, xrow) : before;
-        if (k.c0 < k.c1) {
-            fetch_x(k.c0);
-            st.template fetch_z<0>(k.c0);
-            take_x();
-            st.template put_z<0>(k.c0);
-            fetch_x(k.c0 + 1);
-            st.template fetch_z<0>(k.c0 + 1);
-        }
-        for (int ch = k.c0; ch < k.c1; ++ch) {
-            lds_barrier();
-            // from before the chunk: out^T = S^T x, rows v, columns r; and scores, rows s, columns r
-            f32x16 out[VB], sc = zeros16();
-#pragma unroll
-            for (int vb = 0; vb < VB; ++vb) out[vb] = zeros16();
+        const int on = w == 2 || first < 0 || first % 8 > 2 ? -1 : first / 8;  // the four that the diagonal leaves in part
+        auto scores = [&](int P) {
+            f32x16 sc = zeros16();
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk) {
-                const bf16x8 x = __builtin_bit_cast(bf16x8, xr[kk]);
-                mma32x32(sc, __builtin_bit_cast(bf16x8, t.y[0][at[kk] + w * 32 * RY]), x);
-#pragma unroll
-                for (int vb = 0; vb < VB; ++vb)
-                    mma32x32(out[vb], __builtin_bit_cast(bf16x8, t.s[0][(32 * vb + n) * Stage::RS + 2 * kk + hf]), x);
+                const bf16x4 lo = *((const bf16x4*)(t.y[P] + tile_at<bf16, RK>(yb + n, 2 * kk)) + hf);
+                const bf16x4 hi = *((const bf16x4*)(t.y[P] + tile_at<bf16, RK>(yb + n, 2 * kk + 1)) + hf);
+                mma32x32(sc, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7),
+                         __builtin_bit_cast(bf16x8, t.x[P][tile_at<bf16, RK>(xb + n, 2 * kk + hf)]));
             }
-            if constexpr (FINE) {
-                lds_barrier();
-                lds_barrier();
 #pragma unroll
-                for (int kk = 0; kk < KK; ++kk)
+            for (int kk = 0; kk < 2; ++kk) {
+                bf16x8 pr, rest;
 #pragma unroll
-                    for (int vb = 0; vb < VB; ++vb)
-                        mma32x32(out[vb], __builtin_bit_cast(bf16x8, t.s[0][(32 * vb + n) * Stage::RS + 2 * kk + hf]), __builtin_bit_cast(bf16x8, xr[kk]));
-            }
-            const float f = ch == 0 ? before0 : before;
-#pragma unroll
-            for (int vb = 0; vb < VB; ++vb)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) out[vb][i] *= f;
-            // out^T += z^T scores^T
-            auto add = [&](const f32x16& score, int r0, auto inside) {
-                constexpr bool SELF = decltype(inside)::value;
-#pragma unroll
-                for (int kk = 0; kk < 2; ++kk) {
-                    bf16x8 pr, rest;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int j = 2 * kk + e / 4, i = e % 4;
-                        const float wt = SELF ? j == on ? diag[i] : self[j] * fall[i] : prev[j] * fall[i];
-                        const float x = score[8 * kk + e] * wt;
-                        pr[e] = (bf16)x;
-                        if constexpr (FINE) rest[e] = (bf16)(x - (float)pr[e]);
-                    }
-#pragma unroll
-                    for (int vb = 0; vb < VB; ++vb) {
-                        const bf16x8 z = columns32<RZ>(t.z[0], r0 + 16 * kk, 4 * vb, l);
-                        mma32x32(out[vb], z, pr);
-                        if constexpr (FINE) mma32x32(out[vb], z, rest);
-                    }
+                for (int e = 0; e < 8; ++e) {
+                    const int j = 2 * kk + e / 4, i = e % 4;
+                    const float v = sc[8 * kk + e] * (j == on ? diag[i] : near[j] * fall[i]);
+                    pr[e] = (bf16)v;
+                    if constexpr (FINE) rest[e] = (bf16)(v - (float)pr[e]);
                 }
-            };
-            add(sc, 32 * w, IC<1>{});
-            if (w) {
-                sc = zeros16();
-#pragma unroll
-                for (int kk = 0; kk < KK; ++kk)
-                    mma32x32(sc, __builtin_bit_cast(bf16x8, t.y[0][at[kk]]), __builtin_bit_cast(bf16x8, xr[kk]));
-                add(sc, 0, IC<0>{});
+                t.pr[0][(2 * w + kk) * 64 + l] = __builtin_bit_cast(i32x4, pr);
+                if constexpr (FINE) t.pr[1][(2 * w + kk) * 64 + l] = __builtin_bit_cast(i32x4, rest);
             }
-            put_out(ch, out);
-            if (ch + 1 < k.c1) {
-                take_x();
-                fetch_x(ch + 2);
+        };
+        if (k.c0 < k.c1) {
+            fetch_rows(k.c0);
+            zs.fetch(k.c0);
+            put_rows(0);
+            fetch_rows(k.c0 + 1);
+            split_late(k.c0);
+            zs.fetch(k.c0 + 1);
+            put_late(0);
+            lds_barrier();
+        }
+        for (int ch = k.c0; ch < k.c1; ++ch) {
+            const int P = (ch - k.c0) & 1;
+            if constexpr (LOCAL) {
+                if (ch + 1 < k.c1) {
+                    put_rows(1 - P);
+                    fetch_rows(ch + 2);
+                    split_late(ch + 1);
+                    zs.fetch(ch + 2);
+                    put_late(1 - P);
+                    lds_barrier();
+                }
+            } else {
+                if (w < 3) scores(P);
+                if (ch + 1 < k.c1) {
+                    put_rows(1 - P);
+                    fetch_rows(ch + 2);
+                    split_late(ch + 1);
+                    zs.fetch(ch + 2);
+                }
                 lds_barrier();
-                st.template put_z<0>(ch + 1);
-                st.template fetch_z<0>(ch + 2);
+                if (ch + 1 < k.c1) {
+                    put_late(0);
+                    lds_barrier();
+                }
             }
         }
-        k.pad(threadIdx.x, 128);
+        if constexpr (!LOCAL) k.pad(th, kDlaHelp);
     }
 }
-template <int KM, bool LOCAL, bool FINE>
-__global__ __launch_bounds__(256, LOCAL ? 3 : 2) void gdr2_dla_kernel(DlaParams p, int nwork) {
-    __shared__ i32x4 lds[sizeof(DlaLds<KM ? KM : 128, LOCAL>) / 16];
-    dla_share<KM>(p, nwork, [&](auto k, int item, int ip) { dla_body<decltype(k)::value, LOCAL, FINE>(p, lds, item, ip); });
+// K = 0: a backward whose dk and dv differ, passes of either kind.
+template <int K, int V, bool LOCAL, bool FINE>
+__global__ __launch_bounds__(512, 2) void gdr2_dla_kernel(DlaParams p, int nwork) {
+    constexpr size_t A = sizeof(DlaTiles<K ? K : 128, K ? V : 64, LOCAL, FINE>), B = sizeof(DlaTiles<K ? K : 64, K ? V : 128, LOCAL, FINE>);
+    __shared__ i32x4 lds[(A > B ? A : B) / 16];
+    dla_share<K>(p, nwork, [&](auto k, int item, int ip) {
+        constexpr int KP = decltype(k)::value;
+        dla_body<KP, K ? V : 192 - KP, LOCAL, FINE>(p, lds, item, ip);
+    });
 }
 
 // ------------------------------------------------------------------ fp32
 // 16 x 16 products, of which this type's scores need eight times as many cycles: waves 0..3 read sixteen rows each,
 // waves 4..7 carry every fourth sixteen of the state's rows.
+// Staging of y and z, z also as the decayed operand z_s a^(63 - s) of the state's sums.  Set (ch - c0) % 2 of the registers
+// and of the tiles belongs to chunk ch.  Behind the last chunk nothing is loaded.
 template <int K, bool LOCAL>
-using DlaF32Stage = DlaStage<float, K, kDlaF32VS, LOCAL, LOCAL ? 256 : 512, LOCAL ? 256 : 512, 2>;
+struct DlaF32Stage {
+    typedef DlaWork<float, K, kDlaF32VS, LOCAL> Work;
+    static constexpr int NT = LOCAL ? 256 : 512, RY = Work::RY, RZ = Work::RZ, YU = C * RY / NT, ZU = C * RZ / NT;
+    struct Tiles {
+        i32x4 y[2][C * RY];
+        i32x4 z[LOCAL ? 1 : 2][LOCAL ? 1 : C * RZ];
+        i32x4 d[2][C * RZ];
+        i32x4 s[LOCAL ? 1 : 2][LOCAL ? 1 : kDlaF32VS * RY];  // the state as the chunk reads it, [v][k]
+    };
+    const Work& k;
+    Tiles& t;
+    DlaStream ys, zs;
+    i32x4 yr[2][YU], zr[2][ZU];
+    int th, yo[YU], zo[ZU];
+    float late[ZU];  // a^(63 - s) of the staged rows
+    __device__ __forceinline__ DlaF32Stage(const Work& work, Tiles& tiles, int thread)
+        : k(work), t(tiles), ys(work.rows_of_k(work.ps.y)), zs(work.rows_of_v(work.ps.z)), th(thread) {
+#pragma unroll
+        for (int u = 0; u < YU; ++u) yo[u] = k.off((th + u * NT) / RY, k.sx) + (th + u * NT) % RY * 16;
+#pragma unroll
+        for (int u = 0; u < ZU; ++u) {
+            zo[u] = k.off((th + u * NT) / RZ, k.sz) + (th + u * NT) % RZ * 16;
+            late[u] = dla_pow(k.ga, C - 1 - (th + u * NT) / RZ);
+        }
+    }
+    template <int P>
+    __device__ __forceinline__ void fetch(int ch) {
+        int shift;
+        const auto y = ys.next(ch, shift);
+#pragma unroll
+        for (int u = 0; u < YU; ++u) yr[P][u] = load16(y, yo[u] - shift);
+        const auto z = zs.next(ch, shift);
+#pragma unroll
+        for (int u = 0; u < ZU; ++u) zr[P][u] = load16(z, zo[u] - shift);
+    }
+    template <int P>
+    __device__ __forceinline__ void put(int ch) {
+        const int n = k.L - ch * C;
+#pragma unroll
+        for (int u = 0; u < YU; ++u) t.y[P][tile_at<float, RY>((th + u * NT) / RY, (th + u * NT) % RY)] = yr[P][u];
+#pragma unroll
+        for (int u = 0; u < ZU; ++u) {
+            const int r = (th + u * NT) / RZ, at = tile_at<float, RZ>(r, (th + u * NT) % RZ);
+            if constexpr (!LOCAL) t.z[P][at] = zr[P][u];
+            const float f = n >= C ? late[u] : r < n ? dla_pow(k.ga, n - 1 - r) : 0.f;
+            *(f32x4*)(t.d[P] + at) = __builtin_bit_cast(f32x4, zr[P][u]) * f;
+        }
+    }
+};
 template <int K, bool LOCAL>
 __device__ __forceinline__ void dla_f32_body(const DlaParams& p, i32x4* lds, int item, int ip) {
     typedef DlaWork<float, K, kDlaF32VS, LOCAL> Work;
@@ -595,7 +601,7 @@ __device__ __forceinline__ void dla_f32_body(const DlaParams& p, i32x4* lds, int
         constexpr int R = decltype(pieces)::value;
         return ((const float*)(tile + tile_at<float, R>(row, 4 * block + (c >> 2))))[c & 3];
     };
-    Stage st(k, t, threadIdx.x, threadIdx.x);
+    Stage st(k, t, threadIdx.x);
     if (k.c0 < k.c1) {
         st.template fetch<0>(k.c0);
         st.template fetch<1>(k.c0 + 1);
@@ -656,7 +662,7 @@ __device__ __forceinline__ void dla_f32_body(const DlaParams& p, i32x4* lds, int
                 for (int kb = 0; kb < KB; ++kb) y[kb] = column(t.y[P], IC<RY>{}, r, cw + 4 * kb);
 #pragma unroll
                 for (int vb = 0; vb < VB; ++vb) {
-                    const float z = column(t.d[P][0], IC<RZ>{}, r, vb);
+                    const float z = column(t.d[P], IC<RZ>{}, r, vb);
 #pragma unroll
                     for (int kb = 0; kb < KB; ++kb) mma32(S[kb][vb], y[kb], z);
                 }
@@ -758,20 +764,20 @@ __device__ __forceinline__ void dla_f32_body(const DlaParams& p, i32x4* lds, int
     }
 }
 template <int KM, bool LOCAL>
-__global__ __launch_bounds__(LOCAL ? 256 : 512, 2) void gdr2_dla_f32_kernel(DlaParams p, int nwork) {
+__global__ __launch_bounds__(LOCAL ? 256 : 512, LOCAL ? 1 : 2) void gdr2_dla_f32_kernel(DlaParams p, int nwork) {
     __shared__ i32x4 lds[sizeof(typename DlaF32Stage<KM ? KM : 128, LOCAL>::Tiles) / 16];
     dla_share<KM>(p, nwork, [&](auto k, int item, int ip) { dla_f32_body<decltype(k)::value, LOCAL>(p, lds, item, ip); });
 }
 
-// Segments of the sequence: as many as fill the device once (two workgroups of bf16 to a compute unit, one of fp32), none
-// below four chunks.  Measured for 128 / 256 / 384 / 512 / 768 / 1024 workgroups of bf16: B = 4, T = 4096, H = 16 forward
-// 152 / 140 / 130 / 123 / 131 / 137 us, B = 1, T = 32768, H = 16 467 / 254 / 245 / 225 / 245 / 252 (unsplit 1143); the
-// backward of the first, 384 workgroups in one segment, took 199 us, in two segments 242.  fp32, B = 3, T = 777, H = 6: at least
-// four chunks 29 us against 42 with at least sixteen (one segment); 512 instead of 256 workgroups made its backward 84 us
-// from 76.
+// Segments of the sequence: as many as fill the device once (a workgroup to a compute unit), none below two chunks (fp32:
+// four).  Measured for 192 / 256 / 512 / 768 workgroups of bf16: B = 4, T = 4096, H = 16 forward 114 / 103 / 123 / 134 us,
+// backward 174 / 176 / 218 / 239 (192 workgroups in one segment; then two and four), B = 1, T = 32768, H = 16 214 / 195 / 247 /
+// 263.  At least two, four or eight chunks: B = 1, T = 1000, H = 8 backward 24 / 27 / 39 us.  fp32, B = 3, T = 777, H = 6: at
+// least four chunks 29 us against 42 with at least sixteen (one segment) and 36 with two; 512 instead of 256 workgroups made
+// its backward 84 us from 76.
 DlaCut dla_cut(long B, long T, long H, long slots, bool f32) {
-    const long nch = (T + C - 1) / C, jobs = B * H * slots, least = 4;
-    long segs = jobs > 0 ? (f32 ? 256 : 512) / jobs : 1;
+    const long nch = (T + C - 1) / C, jobs = B * H * slots, least = f32 ? 4 : 2;
+    long segs = jobs > 0 ? 256 / jobs : 1;
     segs = segs < nch / least ? segs : nch / least;
     segs = segs < 1 ? 1 : segs;
     DlaCut c{};
@@ -782,22 +788,24 @@ DlaCut dla_cut(long B, long T, long H, long slots, bool f32) {
     return c;
 }
 
-template <int KM, bool LOCAL>
+template <int K, int V, bool LOCAL>
 static hipError_t launch_dla(bool bf, long n, const DlaParams& p, hipStream_t s) {
-    const dim3 grid((unsigned)((n + 7) / 8 * 8));
-    if (bf && !LOCAL && p.T <= kDlaFine) hipLaunchKernelGGL((gdr2_dla_kernel<KM, false, true>), grid, dim3(256), 0, s, p, (int)n);
-    else if (bf) hipLaunchKernelGGL((gdr2_dla_kernel<KM, LOCAL, false>), grid, dim3(256), 0, s, p, (int)n);
-    else hipLaunchKernelGGL((gdr2_dla_f32_kernel<KM, LOCAL>), grid, dim3(LOCAL ? 256 : 512), 0, s, p, (int)n);
+    const dim3 grid((unsigned)((n + 7) / 8 * 8)), block(kDlaHelp + 64 * (K ? V : 128) / 32);
+    if (bf && !LOCAL && p.T <= kDlaFine) hipLaunchKernelGGL((gdr2_dla_kernel<K, V, false, true>), grid, block, 0, s, p, (int)n);
+    else if (bf) hipLaunchKernelGGL((gdr2_dla_kernel<K, V, LOCAL, false>), grid, block, 0, s, p, (int)n);
+    else hipLaunchKernelGGL((gdr2_dla_f32_kernel<K, LOCAL>), grid, dim3(LOCAL ? 256 : 512), 0, s, p, (int)n);
     return hipGetLastError();
 }
 template <bool LOCAL>
 static hipError_t launch_dla_k(bool bf, long n, const DlaParams& p, hipStream_t s) {
+    const int K = p.pass[0].K, V = p.pass[0].V;
     for (int i = 1; i < p.passes; ++i)
-        if (p.pass[i].K != p.pass[0].K) return launch_dla<0, LOCAL>(bf, n, p, s);
-    return p.pass[0].K == 128 ? launch_dla<128, LOCAL>(bf, n, p, s) : launch_dla<64, LOCAL>(bf, n, p, s);
+        if (p.pass[i].K != K) return launch_dla<0, 0, LOCAL>(bf, n, p, s);
+    if (K == 128) return V == 128 ? launch_dla<128, 128, LOCAL>(bf, n, p, s) : launch_dla<128, 64, LOCAL>(bf, n, p, s);
+    return V == 128 ? launch_dla<64, 128, LOCAL>(bf, n, p, s) : launch_dla<64, 64, LOCAL>(bf, n, p, s);
 }
 
-int dla_slots(int V, bool f32) { return V / (f32 ? kDlaF32VS : kDlaVS); }
+int dla_slots(int V, bool f32) { return f32 ? V / kDlaF32VS : 1; }
 
 hipError_t dla_dispatch(int bf, const DlaParams& p, hipStream_t s) {
     const long per = (long)p.B * p.H * p.slots;  // workgroups of a segment

@@ -60,8 +60,8 @@ static int g_passes;
 // One launch of segments' own states where there are any, then one of everything.
 static void dla_seen(const Launch& l) {
     const auto& p = params<gdr2::DlaParams>(l);
-    const bool local = is(l, "Li0ELb1") || is(l, "Li64ELb1") || is(l, "Li128ELb1");  // <row length or 0, LOCAL, ...>
-    if (is(l, "gdr2_dla_kernel")) CHECK(is(l, "ELb0ELb1E") == (p.T <= 128));         // short sequences' own variant
+    const bool local = is(l, "Li0ELb1") || is(l, "Li64ELb1") || is(l, "Li128ELb1");  // <..., columns or 0, LOCAL, ...>
+    if (is(l, "gdr2_dla_kernel")) CHECK(is(l, "ELb0ELb1E") == (p.T <= 128) && l.block.x >= 256u + 2 * p.pass[0].V);  // short sequences' own variant; waves
     const int64_t per = g_B * g_H * g_slots, n = *(int*)l.args[1];
     CHECK(is(l, "gdr2_dla_") && p.passes == g_passes && p.slots == g_slots && p.T == g_T);
     CHECK(p.segs >= 1 && p.seg_chunks >= 1 && (int64_t)p.segs * p.seg_chunks * 64 >= p.T);
@@ -78,16 +78,16 @@ static void dla() {
         for (gdr2_dtype dt : {GDR2_BF16, GDR2_F32})
             for (int64_t dk : {64, 128})
                 for (int64_t dv : {64, 128}) {
-                    const int64_t wide = dt == GDR2_BF16 ? 64 : 32;
+                    auto slots = [&](int64_t columns) { return dt == GDR2_BF16 ? 1 : columns / 32; };  // workgroups of a pass
                     g_B = c.B, g_T = c.T, g_H = c.H, g_dkdv = dk * dv;
                     g_seen = dla_seen;
                     g_call = text("dla_fwd", {c.B, c.T, c.H, dk, dv, dt});
-                    g_passes = 1, g_slots = dv / wide, g_stage = 0;
+                    g_passes = 1, g_slots = slots(dv), g_stage = 0;
                     size_t n = LIB(gdr2_dla_fwd_workspace_bytes)(c.B, c.T, c.H, dk, dv, dt);
                     CHECK(LIB(gdr2_dla_fwd)(c.B, c.T, c.H, dk, dv, dt, A(0), A(1), A(2), F(3), F(4), I(5), A(6), F(7), W(8, n), n, nullptr) == GDR2_OK);
                     CHECK(g_stage == 2);
                     g_call = text("dla_bwd", {c.B, c.T, c.H, dk, dv, dt});
-                    g_passes = 3, g_slots = (dv + 2 * dk) / wide, g_stage = 0;
+                    g_passes = 3, g_slots = slots(dv) + 2 * slots(dk), g_stage = 0;
                     n = LIB(gdr2_dla_bwd_workspace_bytes)(c.B, c.T, c.H, dk, dv, dt);
                     CHECK(LIB(gdr2_dla_bwd)(c.B, c.T, c.H, dk, dv, dt, A(0), A(1), A(2), F(3), F(4), I(5), A(6), F(7), A(8), A(9), A(10), F(11), W(12, n), n, nullptr) == GDR2_OK);
                     CHECK(g_stage == 2);

@@ -23,7 +23,7 @@ static bool inside(const void* p, size_t n) { return !n || ((uintptr_t)p >= g_ws
 namespace gdr2 {
 // stand-ins for the sizing rules that live beside their kernels
 long rms_bwd_blocks(long rows, int) { return rows < 512 ? rows : 512; }
-int dla_slots(int V, bool f32) { return V / (f32 ? 32 : 64); }
+int dla_slots(int V, bool f32) { return f32 ? V / 32 : 1; }
 DlaCut dla_cut(long B, long T, long H, long slots, bool) {
     const long nch = (T + kDlaChunk - 1) / kDlaChunk, jobs = B * H * slots;
     long n = jobs > 0 ? 300 / jobs : 1;
