@@ -19,7 +19,7 @@
 // products (in short sequences: split in two), whose sums are fp32.  fp32 rounds nothing else.
 //
 // Measured (dk = dv = 128, bf16): B = 4, T = 4096, H = 16 forward 103 us, backward 176 us (its tensors, each once, take 94
-// us at a copy's rate, its 99 GFLOP of products 80 us at the rate of a large one); B = 1, T = 32768, H = 16 195 us, the
+// us at a copy's rate, its 99 GFLOP of products 80 us at the rate of a large one); B = 1, T = 32768, H = 16 195 to 200 us, the
 // bytes of its two launches 168 us.  The chain of steps inside a chunk bounds the backward: the owners' 54 products of 32
 // cycles wait for operands from LDS, each other and two barriers, 5600 cycles a chunk; LDS and the matrix units are 30 % busy.
 // fp32 (B = 3, T = 777, H = 6, dk = 64, dv = 128): forward 29 us, backward 76 us, bound by the fp32 matrix rate: the
