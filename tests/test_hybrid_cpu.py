@@ -54,7 +54,7 @@ def test_dla_abi():
     back = lib.gdr2_dla_bwd_workspace_bytes(1, 4096, 1, 64, 128, 1)
     assert need > 0 and back > 0                                      # few chains: the sequence is cut
     assert lib.gdr2_dla_fwd_workspace_bytes(64, 4096, 16, 128, 128, 1) == 0
-    for bad in ((1, 1 << 31, 1, 64, 64, 1), (1 << 20, 64, 2, 64, 64, 1), (1 << 18, 1 << 20, 1, 64, 64, 1), (-1, 1, 1, 64, 64, 1),
+    for bad in ((1, 1 << 31, 1, 64, 64, 1), (1 << 20, 64, 2, 64, 64, 1), ((1 << 19) + 1, 1, 1, 64, 64, 1), (1 << 18, 1 << 20, 1, 64, 64, 1), (-1, 1, 1, 64, 64, 1),
                 (1, 1, 1, 96, 64, 1), (1, 1, 1, 64, 256, 1), (1, 1, 1, 64, 64, 5)):
         assert lib.gdr2_dla_fwd_workspace_bytes(*bad) == lib.gdr2_dla_bwd_workspace_bytes(*bad) == 0
 
