@@ -54,14 +54,14 @@ def test_dla_abi():
     back = lib.gdr2_dla_bwd_workspace_bytes(1, 4096, 1, 64, 128, 1)
     assert need > 0 and back > 0                                      # few chains: the sequence is cut
     assert lib.gdr2_dla_fwd_workspace_bytes(64, 4096, 16, 128, 128, 1) == 0
-    for bad in ((1, 1 << 31, 1, 64, 64, 1), (1 << 20, 64, 2, 64, 64, 1), ((1 << 19) + 1, 1, 1, 64, 64, 1), (1 << 18, 1 << 20, 1, 64, 64, 1), (-1, 1, 1, 64, 64, 1),
+    for bad in ((1, 1 << 31, 1, 64, 64, 1), (1 << 20, 64, 2, 64, 64, 1), (1 << 18, 1 << 20, 1, 64, 64, 1), (-1, 1, 1, 64, 64, 1),
                 (1, 1, 1, 96, 64, 1), (1, 1, 1, 64, 256, 1), (1, 1, 1, 64, 64, 5)):
         assert lib.gdr2_dla_fwd_workspace_bytes(*bad) == lib.gdr2_dla_bwd_workspace_bytes(*bad) == 0
 
     def fwd(B=1, T=4096, H=1, dk=64, dv=128, dt=1, q=at(0), k=at(1), v=at(2), g=at(3), S0=None, L=None, o=at(4), ST=at(5), ws=at(6), n=need):
         return lib.gdr2_dla_fwd(B, T, H, dk, dv, dt, q, k, v, g, S0, L, o, ST, ws, n, None)
     assert fwd(dt=3) == E_DTYPE and fwd(dk=32) == fwd(dv=96) == E_UNSUP
-    assert fwd(B=-1) == fwd(T=1 << 31) == fwd(B=1 << 21) == fwd(B=1 << 14, H=1 << 5) == fwd(B=1 << 40, H=1 << 40) == E_SHAPE
+    assert fwd(B=-1) == fwd(T=1 << 31) == fwd(B=1 << 21) == fwd(B=(1 << 19) + 1, T=64) == fwd(B=1 << 14, H=1 << 5) == fwd(B=1 << 40, H=1 << 40) == E_SHAPE
     assert fwd(q=None) == fwd(k=None) == fwd(v=None) == fwd(g=None) == fwd(o=None) == E_NULL
     assert fwd(ws=None) == fwd(n=need - 1) == E_WS
     assert fwd(o=at(0)) == fwd(ST=at(4)) == fwd(S0=at(5)) == fwd(ws=at(1)) == fwd(o=at(3)) == E_ALIAS
