@@ -13,10 +13,11 @@
 // the segments' own states (a first launch).  Scores are formed transposed (rows s, columns r), so that a lane's
 // weighted scores are operand values of the next product as they stand, and so are its values of the state.
 //
-// Rounding: S is carried in fp32, its decay as S + S (a^n - 1), so that slow decays lose nothing over long
-// sequences.  For bf16 the decayed operand of its sums is split into bf16 parts: three (24 bits) where the state is a
-// result, two where it is only read, as bf16.  Scores, and S as it is read, are rounded to bf16 once as inputs of their
-// products (in short sequences: split in two), whose sums are fp32.  fp32 rounds nothing else.
+// Rounding: S is carried in fp32, its decay as S + S (a^n - 1) where a^n is above a half, so that slow decays lose nothing over
+// long sequences, and as S a^n below, where a^n - 1 lies next to -1 and its rounding would leave 2^-25 of the old S.  For
+// bf16 the decayed operand of its sums is split into bf16 parts: three (24 bits) where the state is a result, two where it is
+// only read, as bf16.  Scores, and S as it is read, are rounded to bf16 once as inputs of their products (in short sequences:
+// split in two), whose sums are fp32.  fp32 rounds nothing else.
 //
 // Measured (dk = dv = 128, bf16): B = 4, T = 4096, H = 16 forward 103 us, backward 176 us (its tensors, each once, take 94
 // us at a copy's rate, its 99 GFLOP of products 80 us at the rate of a large one); B = 1, T = 32768, H = 16 195 to 200 us, the
@@ -42,6 +43,19 @@ constexpr int kDlaFine = 128;
 
 // a^n for whole n >= 0; a^0 = 1 also where a = 0
 __device__ __forceinline__ float dla_pow(float g, int n) { return n == 0 ? 1.f : expf((float)n * g); }
+
+// The decay of a state over n >= 0 tokens: S a^n, as S + S f (f = a^n - 1) where it is slow, else as S f.
+template <bool SLOW>
+__device__ __forceinline__ float dla_factor(float g, int n) {
+    const float x = (float)n * g;
+    if constexpr (SLOW) return n == 0 ? 0.f : expm1f(x);
+    else return n == 0 ? 1.f : expf(x);
+}
+template <bool SLOW>
+__device__ __forceinline__ float dla_decayed(float s, float f) { return SLOW ? fmaf(s, f, s) : s * f; }
+// Slow: a^n > 1/2.  A head keeps to one form through its chunks, that of a whole one: of shorter ones, which may be slow
+// where a whole one is not, a sequence has two.
+__device__ __forceinline__ bool dla_slow(float g, int n) { return __builtin_amdgcn_readfirstlane(n == 0 || (float)n * g > -0.6931472f); }
 
 // Tiles in LDS are rows of R 16-byte pieces without padding.  Operands with the contraction along a row are read as one
 // piece of sixteen rows, operands with it down the rows as 64 bytes of four rows; an exclusive or on the piece's number
@@ -138,10 +152,21 @@ struct DlaWork {
         return p.local + (((((long)ip * p.B + b) * p.H + h) * (p.segs - 1) + j) * slices + sl) * (K * VS);
     }
     __device__ __forceinline__ bool final_here() const { return nch == 0 ? sg == 0 : c0 < nch && c1 == nch; }
-    // the state's decay over chunk ch less one: S <- S + S (a^n - 1)
+    // The state's decay over chunk ch, where `whole` is a whole one's.  The empty statement keeps the others' behind a branch:
+    // formed in every chunk and then chosen, their exponential lies in the state's way (backward of dk = 128, dv = 64 +18 %).
+    template <bool SLOW>
     __device__ __forceinline__ float decay(int ch, float whole) const {
         const int n = L - ch * C < C ? L - ch * C : C, m = n - (ch == 0 ? early : 0);
-        return m == C ? whole : m == 0 ? 0.f : expm1f((float)m * ga);
+        if (m == C) return whole;
+        asm volatile("");
+        return dla_factor<SLOW>(ga, m);
+    }
+    // f(form, factor) with the decay over segment j
+    template <typename F>
+    __device__ __forceinline__ void segment_decay(int j, F&& f) const {
+        const int n = p.seg_chunks * C - (j == 0 ? early : 0);
+        if (dla_slow(ga, n)) f(IC<1>{}, dla_factor<true>(ga, n));
+        else f(IC<0>{}, dla_factor<false>(ga, n));
     }
     // zeros behind the sequence, in the segment's part of the time axis
     __device__ __forceinline__ void pad(int tid, int threads) const {
@@ -251,8 +276,8 @@ __device__ __forceinline__ void dla_body(const DlaParams& p, i32x4* lds, int ite
     const Work k(p, item, ip);
     if (LOCAL && k.c1 - k.c0 < p.seg_chunks) return;  // no later segment has a token: nobody reads this one's state
     const bool exact = k.ps.state && (LOCAL || k.final_here());
-    auto owner = [&](auto parts) {
-        constexpr int PARTS = decltype(parts)::value;
+    auto owner = [&](auto parts, auto slow) {
+        constexpr int PARTS = decltype(parts)::value, SLOW = decltype(slow)::value;
         const int cv = w - kDlaHelp / 64;
         f32x16 S[KB];  // rows 32 kb + acc_row32(i), columns 32 cv + n
         auto each_four = [&](int j, auto&& f) {  // of the own state of segment j
@@ -261,6 +286,12 @@ __device__ __forceinline__ void dla_body(const DlaParams& p, i32x4* lds, int ite
             for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) f(S[kb], 4 * i, at[((kb * VB + cv) * 4 + i) * 64]);
+        };
+        auto decay_state = [&](auto form, float e) {
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) S[kb][i] = dla_decayed<decltype(form)::value>(S[kb][i], e);
         };
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) S[kb] = zeros16();
@@ -271,10 +302,10 @@ __device__ __forceinline__ void dla_body(const DlaParams& p, i32x4* lds, int ite
 #pragma unroll
                     for (int i = 0; i < 16; ++i) S[kb][i] = k.ps.init[k.state_at(32 * kb + acc_row32(i, l), 32 * cv + n)];
             for (int j = 0; j < k.sg && k.c0 < k.nch; ++j) {
-                const float e = expm1f((float)(p.seg_chunks * C - (j == 0 ? k.early : 0)) * k.ga);
+                k.segment_decay(j, decay_state);
                 each_four(j, [&](f32x16& s, int i0, const f32x4& x) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) s[i0 + i] = fmaf(s[i0 + i], e, s[i0 + i]) + x[i];
+                    for (int i = 0; i < 4; ++i) s[i0 + i] += x[i];
                 });
             }
         }
@@ -288,7 +319,7 @@ __device__ __forceinline__ void dla_body(const DlaParams& p, i32x4* lds, int ite
             before[rb] = dla_pow(k.ga, r + 1);
             before0[rb] = k.early ? dla_pow(k.ga, r) : before[rb];
         }
-        const float whole = expm1f((float)C * k.ga);
+        const float whole = dla_factor<SLOW>(k.ga, C);
         if (k.c0 < k.c1) lds_barrier();
         for (int ch = k.c0; ch < k.c1; ++ch) {
             const int P = (ch - k.c0) & 1;
@@ -321,11 +352,7 @@ __device__ __forceinline__ void dla_body(const DlaParams& p, i32x4* lds, int ite
                     }
                 }
             }
-            const float e = k.decay(ch, whole);
-#pragma unroll
-            for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) S[kb][i] = fmaf(S[kb][i], e, S[kb][i]);
+            decay_state(IC<SLOW>{}, k.template decay<SLOW>(ch, whole));
             bf16x8 y[2][KB], d[2][PARTS];  // operands a step ahead
             auto take = [&](int kk) {
 #pragma unroll
@@ -389,8 +416,13 @@ __device__ __forceinline__ void dla_body(const DlaParams& p, i32x4* lds, int ite
         }
     };
     if (w >= kDlaHelp / 64) {
-        if (exact) owner(IC<3>{});
-        else owner(IC<2>{});
+        if (dla_slow(k.ga, C)) {
+            if (exact) owner(IC<3>{}, IC<1>{});
+            else owner(IC<2>{}, IC<1>{});
+        } else {
+            if (exact) owner(IC<3>{}, IC<0>{});
+            else owner(IC<2>{}, IC<0>{});
+        }
     } else {
         const int th = threadIdx.x;
         DlaRows<RK> xs(k, k.rows_of_k(k.ps.x), k.sx, th), ys(k, k.rows_of_k(k.ps.y), k.sx, th);
@@ -620,6 +652,12 @@ __device__ __forceinline__ void dla_f32_body(const DlaParams& p, i32x4* lds, int
 #pragma unroll
                 for (int vb = 0; vb < VB; ++vb) f(S[kb][vb], 16 * (cw + 4 * kb) + 4 * g, 16 * vb + c, (kb * VB + vb) * 256 + cw * 64 + l);
         };
+        auto decay_state = [&](auto form, float e) {
+            each([&](f32x4& s, int, int, int) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[i] = dla_decayed<decltype(form)::value>(s[i], e);
+            });
+        };
         if constexpr (!LOCAL) {
             if (k.ps.init)
                 each([&](f32x4& s, int row, int v, int) {
@@ -627,33 +665,24 @@ __device__ __forceinline__ void dla_f32_body(const DlaParams& p, i32x4* lds, int
                     for (int i = 0; i < 4; ++i) s[i] = k.ps.init[k.state_at(row + i, v)];
                 });
             for (int j = 0; j < k.sg && k.c0 < k.nch; ++j) {
-                const float e = expm1f((float)(p.seg_chunks * C - (j == 0 ? k.early : 0)) * k.ga);
+                k.segment_decay(j, decay_state);
                 const f32x4* own = (const f32x4*)k.local(j);
-                each([&](f32x4& s, int, int, int at) {
-                    const f32x4 x = own[at];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) s[i] = fmaf(s[i], e, s[i]) + x[i];
-                });
+                each([&](f32x4& s, int, int, int at) { s += own[at]; });
             }
         }
         auto put_state = [&](auto set) {
             constexpr int P = decltype(set)::value;
             if constexpr (!LOCAL) each([&](const f32x4& s, int row, int v, int) { *(f32x4*)(t.s[P] + tile_at<float, RY>(v, row / 4)) = s; });
         };
-        const float whole = expm1f((float)C * k.ga);
         if (k.c0 < k.c1) {
             put_state(IC<0>{});
             st.template put<0>(k.c0);
             st.template fetch<0>(k.c0 + 2);
         }
-        auto chunk = [&](int ch, auto set) {
+        auto chunk = [&](int ch, auto set, auto slow, float whole) {
             constexpr int P = decltype(set)::value;
             lds_barrier();
-            const float e = k.decay(ch, whole);
-            each([&](f32x4& s, int, int, int) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) s[i] = fmaf(s[i], e, s[i]);
-            });
+            decay_state(slow, k.template decay<decltype(slow)::value>(ch, whole));
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
                 const int r = 16 * (j / 4) + 4 * g + j % 4;
@@ -673,10 +702,15 @@ __device__ __forceinline__ void dla_f32_body(const DlaParams& p, i32x4* lds, int
             }
             st.template fetch<1 - P>(ch + 3);
         };
-        for (int ch = k.c0; ch < k.c1; ch += 2) {
-            chunk(ch, IC<0>{});
-            if (ch + 1 < k.c1) chunk(ch + 1, IC<1>{});
-        }
+        auto chunks = [&](auto slow) {
+            const float whole = dla_factor<decltype(slow)::value>(k.ga, C);
+            for (int ch = k.c0; ch < k.c1; ch += 2) {
+                chunk(ch, IC<0>{}, slow, whole);
+                if (ch + 1 < k.c1) chunk(ch + 1, IC<1>{}, slow, whole);
+            }
+        };
+        if (dla_slow(k.ga, C)) chunks(IC<1>{});
+        else chunks(IC<0>{});
         if constexpr (LOCAL) {
             f32x4* own = (f32x4*)k.local(k.sg);
             each([&](const f32x4& s, int, int, int at) { own[at] = s; });
