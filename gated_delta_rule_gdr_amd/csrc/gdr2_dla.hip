@@ -850,7 +850,9 @@ hipError_t dla_dispatch(int bf, const DlaParams& p, hipStream_t s) {
     return launch_dla_k<false>(bf, per * p.segs, p, s);
 }
 
-// One token: S <- a S + k v^T, o = S^T q.  A pure stream over the fp32 state, in registers, 16-byte accesses.
+// One token: S <- a S + k v^T, o = S^T q.  A pure stream over the fp32 state, in registers, 16-byte accesses.  Slow decays are
+// added as S (a - 1): a itself, rounded, would be off to the same side at every token, by up to 2^-25 of S (10000 tokens at
+// log_decay -1e-4: 2500 half steps of the state, against 25).
 template <typename T, int DK, int DV>
 __global__ __launch_bounds__(kDlaThreads) void gdr2_dla_step_kernel(DlaStepParams p) {
     constexpr int CG = DV / 4, RG = kDlaThreads / CG, R = DK / RG;  // column groups, row groups, rows of a thread
@@ -862,7 +864,9 @@ __global__ __launch_bounds__(kDlaThreads) void gdr2_dla_step_kernel(DlaStepParam
     f32x4 s[R];
 #pragma unroll
     for (int u = 0; u < R; ++u) s[u] = p.S_in ? *(const f32x4*)(p.S_in + at + (ig * R + u) * DV) : f32x4{0, 0, 0, 0};
-    const float a = expf(p.log_decay[n % p.H]);
+    const float ga = p.log_decay[n % p.H];
+    const bool slow = dla_slow(ga, 1);
+    const float f = slow ? dla_factor<true>(ga, 1) : dla_factor<false>(ga, 1);
     const f32x4 vv = load4(v + 4 * jg);
     f32x4 o = {0, 0, 0, 0};
 #pragma unroll
@@ -871,7 +875,8 @@ __global__ __launch_bounds__(kDlaThreads) void gdr2_dla_step_kernel(DlaStepParam
         const float ki = to_f(k[i]), qi = to_f(q[i]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            s[u][j] = fmaf(a, s[u][j], ki * vv[j]);
+            const float x = fmaf(f, s[u][j], ki * vv[j]);
+            s[u][j] = slow ? s[u][j] + x : x;
             o[j] = fmaf(qi, s[u][j], o[j]);
         }
         *(f32x4*)(p.S_out + at + i * DV) = s[u];

@@ -76,3 +76,28 @@ def test_dla_carried_state_over_segments(dtype, dk, dv, g):
     assert g2.dla_fwd_workspace_bytes(1, 1024, 8, dk, dv, DT[dtype]) > 0 and g2.dla_bwd_workspace_bytes(1, 1024, 8, dk, dv, DT[dtype]) > 0
     _check(dtype, 1024, dk, dv, g, None, 0)
     _check(dtype, 1024, dk, dv, g, [1001], 40)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_dla_many_steps_do_not_drift(dtype):
+    """Slow decays over 10000 tokens, one by one, whose factors lie half a step of fp32 between two numbers: a rounded factor would be
+    off by 2^-25 at every token, to one side, 2500 to 3000 u32 of the state in the end.  What remains are the two roundings that
+    every step adds to the state, of either sign: sqrt(2 N / 3) u32 of a state that only grows; 4 sqrt(N) u32 leaves a
+    factor of five (e^g - 1 itself, two u32 of it, adds 2 N |g| u32 < 2).  A prefill of the same tokens is as exact."""
+    N, H, dk, dv = 10000, 4, 64, 64
+    announce(f"dla {N} steps {dtype}")
+    gen = torch.Generator().manual_seed(3)
+    g = torch.tensor([-(j + 0.5) * 2.0 ** -24 for j in (1677, 500, 100, 16)])
+    q = (dk ** -0.5 * randn(gen, (1, N, H, dk))).to(DT[dtype])
+    k, v, S0 = (0.1 * randn(gen, (1, N, H, dk))).to(DT[dtype]), randn(gen, (1, N, H, dv), dtype), randn(gen, (1, H, dk, dv))
+    qd, kd, vd, gd, S = (t.to(DEV) for t in (q, k, v, g, S0))
+    _, ST = g2.gdr2_dla_fwd(qd, kd, vd, gd, S)
+    S = S.clone()
+    for t in range(N):
+        g2.gdr2_dla_step(qd[:, t], kd[:, t], vd[:, t], gd, S)
+    a, ref = torch.exp(g.double())[:, None, None], S0[0].double()
+    for kt, vt in zip(k[0].double(), v[0].double()):
+        ref = a * ref + kt[:, :, None] * vt[:, None, :]
+    for name, got in (("steps", S), ("prefill", ST)):
+        err = (got[0].cpu().double() - ref).flatten(1).norm(dim=1) / ref.flatten(1).norm(dim=1)
+        assert (err <= 4 * N ** 0.5 * 2.0 ** -24).all(), f"{name}: {(err * 2 ** 24).tolist()} u32"
