@@ -35,8 +35,8 @@ constexpr int kDlaThreads = 256, C = kDlaChunk;
 // a workgroup, two waves for the outputs, two for the state and that read from LDS, two workgroups to a compute unit, forward
 // and backward of B = 4, T = 4096, H = 16 took 112 + 198 us against 103 + 176, a prompt of 32768 207 against 195.)
 constexpr int kDlaF32VS = 32;
-// Up to this length bf16 keeps 16 bits of the scores and of the state as it is read (two products each): sums that short do
-// not average roundings out.  Normwise error over that of the exact result rounded once, 1 to 64 tokens of a few
+// In sequences of up to this length bf16 keeps 16 bits of the scores and of the state as it is read (two products each): sums
+// that short do not average roundings out.  Normwise error over that of the exact result rounded once, 1 to 64 tokens of a few
 // heads: 1.0 against up to 1.96; from 129 tokens on it is 1.41 to 1.44 with one rounding each.  It costs 64 prompts of 128 tokens
 // (H = 16, dk = dv = 128) 67 us for 60, their backward 133 for 119; fewer chains less than a microsecond.
 constexpr int kDlaFine = 128;
@@ -102,6 +102,12 @@ struct DlaStream {
     }
 };
 
+// Sequence b's length; wave-uniform, for the descriptors
+__device__ __forceinline__ int dla_length(const DlaParams& p, int b) {
+    const int n = p.lengths ? p.lengths[b] : p.T;
+    return __builtin_amdgcn_readfirstlane(n < 0 ? 0 : n > p.T ? p.T : n);
+}
+
 // A workgroup's share: VS columns of one pass of one chain, chunks c0 .. c1 - 1 of the sequence.  Row r of chunk ch is
 // token 64 ch + r, or L - 1 - (64 ch + r) against time.
 template <typename T, int K, int VS, bool LOCAL>
@@ -125,8 +131,7 @@ struct DlaWork {
         sl = item % p.slots - ps.slot, sg = item / p.slots % segs;
         const int bh = item / p.slots / segs;
         h = bh % p.H, b = bh / p.H;
-        const int n = p.lengths ? p.lengths[b] : p.T;
-        L = __builtin_amdgcn_readfirstlane(n < 0 ? 0 : n > p.T ? p.T : n);  // wave-uniform, for the descriptors
+        L = dla_length(p, b);
         nch = (L + C - 1) / C, c0 = sg * p.seg_chunks;
         c1 = c0 + p.seg_chunks < nch ? c0 + p.seg_chunks : nch;
         ga = uniform(p.log_decay[h]);
@@ -564,6 +569,20 @@ __global__ __launch_bounds__(512, 2) void gdr2_dla_kernel(DlaParams p, int nwork
     });
 }
 
+// A padded batch of more: each sequence's variant by its own length, so that its result does not depend on its company.  The
+// second variant's registers and LDS cost the others 0 to 4 % (B = 4, T = 4096, H = 16, dk = dv = 128, lengths from 4096 to 2048:
+// forward 90 -> 91 us, backward 167 -> 170).
+template <int K, int V>
+__global__ __launch_bounds__(512, 2) void gdr2_dla_ragged_kernel(DlaParams p, int nwork) {
+    constexpr size_t A = sizeof(DlaTiles<K ? K : 128, K ? V : 64, false, true>), B = sizeof(DlaTiles<K ? K : 64, K ? V : 128, false, true>);
+    __shared__ i32x4 lds[(A > B ? A : B) / 16];
+    dla_share<K>(p, nwork, [&](auto k, int item, int ip) {
+        constexpr int KP = decltype(k)::value, VP = K ? V : 192 - KP;
+        if (dla_length(p, item / p.slots / p.segs / p.H) <= kDlaFine) dla_body<KP, VP, false, true>(p, lds, item, ip);
+        else dla_body<KP, VP, false, false>(p, lds, item, ip);
+    });
+}
+
 // ------------------------------------------------------------------ fp32
 // 16 x 16 products, of which this type's scores need eight times as many cycles: waves 0..3 read sixteen rows each,
 // waves 4..7 carry every fourth sixteen of the state's rows.
@@ -826,6 +845,7 @@ template <int K, int V, bool LOCAL>
 static hipError_t launch_dla(bool bf, long n, const DlaParams& p, hipStream_t s) {
     const dim3 grid((unsigned)((n + 7) / 8 * 8)), block(kDlaHelp + 64 * (K ? V : 128) / 32);
     if (bf && !LOCAL && p.T <= kDlaFine) hipLaunchKernelGGL((gdr2_dla_kernel<K, V, false, true>), grid, block, 0, s, p, (int)n);
+    else if (bf && !LOCAL && p.lengths) hipLaunchKernelGGL((gdr2_dla_ragged_kernel<K, V>), grid, block, 0, s, p, (int)n);
     else if (bf) hipLaunchKernelGGL((gdr2_dla_kernel<K, V, LOCAL, false>), grid, block, 0, s, p, (int)n);
     else hipLaunchKernelGGL((gdr2_dla_f32_kernel<K, LOCAL>), grid, dim3(LOCAL ? 256 : 512), 0, s, p, (int)n);
     return hipGetLastError();

@@ -558,7 +558,8 @@ gdr2_status gdr2_rms_norm_q8_fwd(int64_t rows, int64_t D, gdr2_dtype dtype, int6
  * [N][H][dk][dv] fp32 (NULL = zero; may equal S_out exactly); N H < 2^24.
  * Precision: states and every sum are fp32.  With GDR2_BF16 a decayed operand of the state's sums keeps 24
  * bits in S_T and dS0 and 16 in states that are only read; scores and the states as read are rounded to bf16 once
- * each, as inputs of the matrix products, but for T <= 128, where they keep 16 bits.
+ * each, as inputs of the matrix products, but in sequences of up to 128 tokens (their own, not the padding's), where
+ * they keep 16 bits.
  * A NaN or infinity stays in its sequence and head (products are formed over tiles: there it may also reach
  * rows before it).
  */
