@@ -20,7 +20,8 @@
 namespace gdr2 {
 
 constexpr int kPagedThreads = 256, kPagedWaves = 4, kPagedTile = kPagedStep / kPagedWaves;
-constexpr float kPagedLowest = -3.0e38f, kPagedLog2e = 1.4426950408889634f;
+// Maxima start at the lowest finite number: below every finite score, and a masked one, -inf, leaves exp2(-inf) = 0 of it.
+constexpr float kPagedLowest = -__FLT_MAX__, kPagedLog2e = 1.4426950408889634f;
 
 // What a sequence sees: positions 0 .. old - 1 through the table, then the new token.  Parts of whole steps.
 struct PagedSeq {
