@@ -112,8 +112,7 @@ __device__ __forceinline__ int dla_length(const DlaParams& p, int b) {
 // token 64 ch + r, or L - 1 - (64 ch + r) against time.
 template <typename T, int K, int VS, bool LOCAL>
 struct DlaWork {
-    static constexpr int ES = (int)sizeof(T), E16 = 16 / ES;     // elements of a 16-byte piece
-    static constexpr int RY = K * ES / 16, RZ = VS * ES / 16;    // pieces of a row
+    static constexpr int ES = (int)sizeof(T), RY = K * ES / 16, RZ = VS * ES / 16;    // pieces of a row
     const DlaParams& p;
     const DlaPass& ps;
     int V, slices, ip, sl, sg, h, b;

@@ -57,7 +57,7 @@ gdr2_status rms_fwd(gdr2::RmsKind kind, int64_t rows, int64_t D, gdr2_dtype dt, 
 
 // ------------------------------------------------------------------ linear attention with a decay per head
 // Afterwards B * H <= 2^19, B * T * H <= 2^30, and every launch fits: at most twelve workgroups of 512 threads per
-// chain, or (few chains) at most 512 in all.
+// chain, or (few chains, cut into segments) at most 256 in all.
 gdr2_status check_dla(int64_t B, int64_t T, int64_t H, int64_t dk, int64_t dv) {
     if (B < 0 || T < 0 || H < 0 || dk < 0 || dv < 0 || T > ((int64_t)1 << 30) || H > 32768) return GDR2_E_SHAPE;
     if (!dims_ok(dk) || !dims_ok(dv)) return GDR2_E_UNSUPPORTED;

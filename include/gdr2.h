@@ -110,7 +110,7 @@ typedef enum gdr2_gates {
  *     q <- q / sqrt(sum_i q_i^2 + norm_eps),   k <- k / sqrt(sum_i k_i^2 + norm_eps)
  *     b <- sigmoid(b),   w <- sigmoid(w),   log_alpha <- -decay_scale * softplus(log_alpha)
  * and the backward returns dq, dk, dlog_alpha, db and dw with respect to those pre-activations
- * (v and dv are unchanged).  Both parameters must be > 0 and finite (else GDR2_E_VALUE).
+ * (v and dv are unchanged).  Both parameters must be > 0 and below 1e30 (else GDR2_E_VALUE).
  */
 typedef struct gdr2_prologue {
     float decay_scale;
@@ -359,7 +359,7 @@ gdr2_status gdr2_decode_step_ex(int64_t N, int64_t H, int64_t dk, int64_t dv, gd
  * with one weight vector shared by all heads.
  *   o, g, y         [rows][dv]  dtype       (o: the mixer output, g: gate pre-activation; y: output)
  *   weight          [dv]        fp32
- *   eps             > 0, finite (else GDR2_E_VALUE)
+ *   eps             > 0, below 1e30 (else GDR2_E_VALUE)
  * The backward takes dy [rows][dv] and writes do_, dg [rows][dv] (dtype) and dweight [dv] (fp32,
  * the sum over all rows, reduced in a fixed order: bitwise deterministic); it needs a workspace
  * of gdr2_out_gate_bwd_workspace_bytes(rows, dv) bytes.  dv in {64, 128}; rows <= 2^37
@@ -398,7 +398,7 @@ gdr2_status gdr2_out_gate_bwd(int64_t rows, int64_t dv, gdr2_dtype dtype, const 
  *   x, y, dy, dx    [rows][D]  dtype
  *   weight, bias    [D]        fp32   (bias NULL = none)
  *   mean, rstd      [rows]     fp32   (forward outputs, NULL = not wanted; the backward reads them)
- *   eps             > 0, finite (else GDR2_E_VALUE)
+ *   eps             > 0, below 1e30 (else GDR2_E_VALUE)
  * The backward writes dx, dweight and dbias (NULL = not wanted), [D] fp32 sums over all rows added
  * in a fixed order (zero for rows = 0).
  */
@@ -451,7 +451,7 @@ gdr2_status gdr2_glr_step(int64_t N, int64_t D, gdr2_dtype dtype, const void* x,
  *   lengths         [B] int32 or NULL (every sequence has T tokens); values are clamped to [0, T].
  *                   Rows at and behind the length are padding: o, dq, dk, dv are zero there, lse -inf
  *   lse             [B][H][T] fp32 (natural log)
- *   window          >= 1;  0 <= sinks <= 64;  scale > 0, finite (else GDR2_E_VALUE)
+ *   window          >= 1;  0 <= sinks <= 64;  scale > 0, below 1e30 (else GDR2_E_VALUE)
  * The backward takes the forward's o and lse.  dk and dv are summed over the heads that share them.
  * Precision: scores, softmax statistics and every sum are fp32 for both dtypes.  GDR2_F32 rounds nothing else.
  * With GDR2_BF16 the probabilities (forward, backward and decode) and the score gradients are each rounded to bf16
@@ -513,7 +513,7 @@ gdr2_status gdr2_swa_decode_step(int64_t N, int64_t H, int64_t Hkv, int64_t d, g
  *                                          otherwise h is required and may be residual exactly
  *   weight              [D]        fp32
  *   rstd                [rows]     fp32 or NULL (not wanted; the backward reads it)
- *   eps                 > 0, finite (else GDR2_E_VALUE)
+ *   eps                 > 0, below 1e30 (else GDR2_E_VALUE)
  * The backward takes the stream h (x without a residual), dy [rows][D] and the stream's own cotangent dh
  * [rows][D] (NULL = zero) and writes dx [rows][D], which is the gradient of x and of residual alike, and
  * dweight [D] fp32, added over all rows in a fixed order (zero for rows = 0):
@@ -596,7 +596,7 @@ gdr2_status gdr2_dla_step(int64_t N, int64_t H, int64_t dk, int64_t dv, gdr2_dty
  * attention output o ([N][H][d]) over the positions 0 .. pos[n]; the new token sees itself whether it has a
  * row or not.  Query head h reads key/value head h / (H / Hkv).  A negative pos[n] means that sequence has no
  * token: o is zero, nothing is stored.
- *   H a multiple of Hkv, H <= 32768, d in {64, 128}, N * H <= 2^30, B * T * Hkv <= 2^32; scale > 0, finite
+ *   H a multiple of Hkv, H <= 32768, d in {64, 128}, N * H <= 2^30, B * T * Hkv <= 2^32; scale > 0, below 1e30
  *   workspace   gdr2_paged_decode_workspace_bytes() bytes (0: none needed)
  * Precision: fp32 throughout; with GDR2_BF16 the probabilities keep 16 bits as inputs of their product.  A value
  * that is not finite at a position that a token sees makes that channel of its heads infinite or NaN, no other.
