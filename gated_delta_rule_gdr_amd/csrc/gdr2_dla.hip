@@ -19,11 +19,12 @@
 // only read, as bf16.  Scores, and S as it is read, are rounded to bf16 once as inputs of their products (in short sequences:
 // split in two), whose sums are fp32.  fp32 rounds nothing else.
 //
-// Measured (dk = dv = 128, bf16): B = 4, T = 4096, H = 16 forward 103 us, backward 176 us (its tensors, each once, take 94
-// us at a copy's rate, its 99 GFLOP of products 80 us at the rate of a large one); B = 1, T = 32768, H = 16 195 to 200 us, the
-// bytes of its two launches 168 us.  The chain of steps inside a chunk bounds the backward: the owners' 54 products of 32
-// cycles wait for operands from LDS, each other and two barriers, 5600 cycles a chunk; LDS and the matrix units are 30 % busy.
-// fp32 (B = 3, T = 777, H = 6, dk = 64, dv = 128): forward 29 us, backward 76 us, bound by the fp32 matrix rate: the
+// Measured in whole calls (dk = dv = 128, bf16): B = 4, T = 4096, H = 16 forward 103 us, backward 176 us (its tensors, each
+// once, take 94 us at a copy's rate, its 99 GFLOP of products 80 us at the rate of a large one; traced launches of both are
+// a tenth longer); B = 1, T = 32768, H = 16 194 to 200 us, the bytes of its two launches 168 us.  The chain of steps inside a
+// chunk bounds the backward: the owners' 54 products of 32 cycles wait for operands from LDS, each other and two barriers, 5600
+// cycles a chunk; the matrix units are busy for 25 % of the launch, the LDS pipe for 23 %.
+// fp32 (B = 3, T = 777, H = 6, dk = 64, dv = 128): forward 30 us, backward 78 us, bound by the fp32 matrix rate: the
 // busiest of four SIMDs has 288 products of 32 cycles per chunk, 9200 of its 13000 cycles.
 #include "gdr2_common.hpp"
 #include "gdr2_hybrid_kernels.hpp"

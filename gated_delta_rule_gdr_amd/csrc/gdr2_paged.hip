@@ -251,13 +251,14 @@ __global__ __launch_bounds__(kPagedThreads) void gdr2_paged_join_kernel(PagedDec
     store4((T*)p.o + ((long)sq * p.H + head) * D + 4 * ln, o * (1.f / Z));
 }
 
-// Parts of the positions: as many as make 2048 workgroups with their sequences and heads, none below a step of 128.
+// Parts of the positions, by the table's width: only the device knows how many of them a sequence holds, and it spreads
+// their steps over the parts.  As many as make 2048 workgroups with the sequences and heads, none below a step of 128.
 // That is more than the device holds at once: lengths differ, and so do the parts' ends.  Measured for 256 / 512 / 1024 /
 // 2048 / 4096 workgroups (16 query heads over 4 of d = 128, bf16): 256 sequences of 1 to 4096 positions 219 / 219 / 219 /
 // 208 / 206 us, one of 32768 18 / 18 / 21 / 21 / 21, 32 of 1 to 4096 40 / 31 / 33 / 32 / 40; and 13 of 1 to 2777, fp32,
-// 12 over 4 heads of d = 64, 20 / 19 / 17 / 14.5 / 15.  Up to three steps stay one part, since the launch that joins parts
-// costs as much as two steps: 64 sequences of 300 positions 7.7 us in one part each, 10.3 in three; one of 500 (four steps)
-// 7.5 us in four parts, 9.1 in two.
+// 12 over 4 heads of d = 64, 20 / 19 / 17 / 14.5 / 15.  Tables of up to three steps stay one part, since the launch that joins
+// parts costs as much as two steps: 64 sequences of 300 positions 7.7 us in one part each, 10.3 in three (as a wider table has
+// them); one of 500 (four steps) 7.5 us in four parts, 9.1 in two.
 int paged_splits(long N, long Hkv, long groups, long capacity) {
     const long jobs = N * Hkv * groups, steps = (capacity + kPagedStep) / kPagedStep;  // the new token included
     if (steps <= 3 || jobs < 1 || jobs > 1024) return 1;
