@@ -19,9 +19,9 @@
 // only read, as bf16.  Scores, and S as it is read, are rounded to bf16 once as inputs of their products (in short sequences:
 // split in two), whose sums are fp32.  fp32 rounds nothing else.
 //
-// Measured in whole calls (dk = dv = 128, bf16): B = 4, T = 4096, H = 16 forward 103 us, backward 176 us (its tensors, each
+// Measured in whole calls (dk = dv = 128, bf16): B = 4, T = 4096, H = 16 forward 98 us, backward 171 us (its tensors, each
 // once, take 94 us at a copy's rate, its 99 GFLOP of products 80 us at the rate of a large one; traced launches of both are
-// a tenth longer); B = 1, T = 32768, H = 16 194 to 200 us, the bytes of its two launches 168 us.  The chain of steps inside a
+// a tenth longer); B = 1, T = 32768, H = 16 191 us, the bytes of its two launches 168 us.  The chain of steps inside a
 // chunk bounds the backward: the owners' 54 products of 32 cycles wait for operands from LDS, each other and two barriers, 5600
 // cycles a chunk; the matrix units are busy for 25 % of the launch, the LDS pipe for 23 %.
 // fp32 (B = 3, T = 777, H = 6, dk = 64, dv = 128): forward 30 us, backward 78 us, bound by the fp32 matrix rate: the
@@ -148,9 +148,12 @@ struct DlaWork {
     }
     __device__ __forceinline__ DlaStream rows_of_k(const void* t) const { return stream(t, sx, K * ES, K, 0); }
     __device__ __forceinline__ DlaStream rows_of_v(const void* t) const { return stream(t, sz, VS * ES, V, sl * VS); }
-    // the number (k, column v of the slice) of the chain's state in memory
-    __device__ __forceinline__ long state_at(int k, int v) const {
-        return ((long)b * p.H + h) * K * V + (ps.flip ? (long)(sl * VS + v) * K + k : (long)k * V + sl * VS + v);
+    // The number (k, column v of the slice) of the chain's state in memory, whose steps along k and v are chosen once for all
+    // of a lane's numbers.
+    __device__ __forceinline__ int step_k() const { return ps.flip ? 1 : V; }
+    __device__ __forceinline__ int step_v() const { return ps.flip ? K : 1; }
+    __device__ __forceinline__ long state_at(int k, int v, int sk, int sv) const {
+        return ((long)b * p.H + h) * K * V + k * sk + (sl * VS + v) * sv;
     }
     // the own state of segment j
     __device__ __forceinline__ float* local(int j) const {
@@ -284,6 +287,9 @@ __device__ __forceinline__ void dla_body(const DlaParams& p, i32x4* lds, int ite
     auto owner = [&](auto parts, auto slow) {
         constexpr int PARTS = decltype(parts)::value, SLOW = decltype(slow)::value;
         const int cv = w - kDlaHelp / 64;
+        // unknown to the compiler: it would form all instances' addresses before choosing among them, more than fit the registers
+        int sk = k.step_k(), sv = k.step_v();
+        asm volatile("" : "+s"(sk), "+s"(sv));
         f32x16 S[KB];  // rows 32 kb + acc_row32(i), columns 32 cv + n
         auto each_four = [&](int j, auto&& f) {  // of the own state of segment j
             f32x4* at = (f32x4*)k.local(j) + l;
@@ -305,7 +311,7 @@ __device__ __forceinline__ void dla_body(const DlaParams& p, i32x4* lds, int ite
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) S[kb][i] = k.ps.init[k.state_at(32 * kb + acc_row32(i, l), 32 * cv + n)];
+                    for (int i = 0; i < 16; ++i) S[kb][i] = k.ps.init[k.state_at(32 * kb + acc_row32(i, l), 32 * cv + n, sk, sv)];
             for (int j = 0; j < k.sg && k.c0 < k.nch; ++j) {
                 k.segment_decay(j, decay_state);
                 each_four(j, [&](f32x16& s, int i0, const f32x4& x) {
@@ -417,7 +423,7 @@ __device__ __forceinline__ void dla_body(const DlaParams& p, i32x4* lds, int ite
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) k.ps.fin[k.state_at(32 * kb + acc_row32(i, l), 32 * cv + n)] = S[kb][i] * f;
+                for (int i = 0; i < 16; ++i) k.ps.fin[k.state_at(32 * kb + acc_row32(i, l), 32 * cv + n, sk, sv)] = S[kb][i] * f;
         }
     };
     if (w >= kDlaHelp / 64) {
@@ -660,6 +666,7 @@ __device__ __forceinline__ void dla_f32_body(const DlaParams& p, i32x4* lds, int
     if (LOCAL || w >= 4) {
         // blocks of 16 x 16: rows 16 (cw + 4 kb) + 4 g + i, column 16 vb + c
         const int cw = LOCAL ? w : w - 4;
+        const int sk = k.step_k(), sv = k.step_v();
         f32x4 S[KB][VB];
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
@@ -681,7 +688,7 @@ __device__ __forceinline__ void dla_f32_body(const DlaParams& p, i32x4* lds, int
             if (k.ps.init)
                 each([&](f32x4& s, int row, int v, int) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) s[i] = k.ps.init[k.state_at(row + i, v)];
+                    for (int i = 0; i < 4; ++i) s[i] = k.ps.init[k.state_at(row + i, v, sk, sv)];
                 });
             for (int j = 0; j < k.sg && k.c0 < k.nch; ++j) {
                 k.segment_decay(j, decay_state);
@@ -737,7 +744,7 @@ __device__ __forceinline__ void dla_f32_body(const DlaParams& p, i32x4* lds, int
             const float f = k.rev && k.L > 0 ? dla_pow(k.ga, 1) : 1.f;
             each([&](const f32x4& s, int row, int v, int) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) k.ps.fin[k.state_at(row + i, v)] = s[i] * f;
+                for (int i = 0; i < 4; ++i) k.ps.fin[k.state_at(row + i, v, sk, sv)] = s[i] * f;
             });
         }
     } else if constexpr (!LOCAL) {
